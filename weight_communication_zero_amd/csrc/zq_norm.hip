@@ -1,0 +1,309 @@
+// zq_norm.hip -- the global norm of many gradient tensors, and clipping by it.
+//   sumsq = [sumsq +] sum over all tensors of x * x            (binary64)
+//   norm = sqrt(sumsq);  c = fl32(min(1, max_norm / (norm + eps)))
+//   out = fl(c * x), rounded to nearest even in a 16-bit type
+//
+// The sum is binary64 from the first product on: a binary32 value's square is
+// exact there and cannot overflow, and the order of the additions (tiles dealt
+// round robin to a fixed number of waves, a tree in the wave and the
+// workgroup, the workgroups' partials in a fixed order) depends on the
+// segments' sizes alone, so equal inputs give equal bits.  The sum reads
+// 4 / 2 B/elem, the clip reads and writes them.  No atomics.
+#include <algorithm>
+
+#include "zq_rows.h"
+
+namespace zq {
+namespace {
+
+constexpr int kNormSegs = 128;  // two table entries per lane (SegmentFinder)
+constexpr int kNormU = 4;
+constexpr uint32_t kNormMaxWgs = 2048;
+constexpr uint32_t kNormOneWg = 64;  // most tiles that one workgroup sums by itself
+
+// A tile is 64 lanes x kNormU 16-byte vectors.
+template <int T>
+struct NormGeom {
+    static constexpr int VEC = T == kF32 ? 4 : 8;
+    static constexpr int SUB = kWave * VEC;
+    static constexpr int TILE = SUB * kNormU;
+};
+
+template <int T>
+__device__ __forceinline__ void widen(u4 w, float* x) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (T == kF32) {
+            x[i] = bitsf(v[i]);
+        } else {
+            x[2 * i] = half_lo<T>(v[i]);
+            x[2 * i + 1] = half_hi<T>(v[i]);
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ float load1(const void* p, uint64_t i) {
+    if constexpr (T == kF32)
+        return ((const float*)p)[i];
+    else
+        return half_lo<T>(((const uint16_t*)p)[i]);
+}
+
+struct NormBatch {
+    const void* g[kNormSegs];
+    uint64_t n[kNormSegs];
+    uint32_t tile_end[kNormSegs];  // cumulative tiles; unused entries hold UINT32_MAX
+    uint32_t total;
+};
+
+// Sum over the wave's lanes, the same tree on every call; lane 0 has it.
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        v += __shfl_down(v, d);
+    return v;
+}
+
+// Sum over the workgroup; thread 0 has it.
+__device__ __forceinline__ double group_sum(double v) {
+    __shared__ double part[16];
+    v = wave_sum(v);
+    if (lane_id() == 0)
+        part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (uint32_t w = 1; w < blockDim.x >> 6; ++w)
+            v += part[w];
+    return v;
+}
+
+// out: one partial per workgroup, or (last) the result itself.
+template <int T>
+__global__ __launch_bounds__(1024) void sumsq_kernel(NormBatch b, double* out, uint32_t last,
+                                                     uint32_t accumulate) {
+    using G = NormGeom<T>;
+    const SegmentFinder<kNormSegs> find(b.tile_end, (uint32_t)kNormSegs);
+    const int lane = lane_id();
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    for (size_t ts = wave_id(); ts < b.total; ts += wave_count()) {
+        const uint32_t t = (uint32_t)ts, s = find(t);
+        const uint64_t base = (uint64_t)(t - (s ? b.tile_end[s - 1] : 0u)) * G::TILE;
+        const void* g = b.g[s];
+        const uint64_t n = b.n[s];
+        if (base + G::TILE <= n) {
+            u4 w[kNormU];
+#pragma unroll
+            for (int u = 0; u < kNormU; ++u) {
+                const uint64_t i0 = base + (uint64_t)u * G::SUB + (uint64_t)lane * G::VEC;
+                w[u] = ld_stream((const u4*)((const char*)g + i0 * (16 / G::VEC)));
+            }
+#pragma unroll
+            for (int u = 0; u < kNormU; ++u) {
+                float x[G::VEC];
+                widen<T>(w[u], x);
+#pragma unroll
+                for (int j = 0; j < G::VEC; ++j)
+                    acc[j & 3] = __builtin_fma((double)x[j], (double)x[j], acc[j & 3]);
+            }
+        } else {
+            for (uint64_t i = base + lane; i < n; i += kWave) {
+                const double x = (double)load1<T>(g, i);
+                acc[0] = __builtin_fma(x, x, acc[0]);
+            }
+        }
+    }
+    const double v = group_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    if (threadIdx.x == 0) {
+        if (last)
+            *out = accumulate ? *out + v : v;
+        else
+            out[blockIdx.x] = v;
+    }
+}
+
+// Joins the workgroups' partials: one workgroup, a fixed order.
+__global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* __restrict__ part,
+                                                          uint64_t n, double* sumsq,
+                                                          uint32_t accumulate) {
+    double a = 0.0;
+    for (uint64_t i = threadIdx.x; i < n; i += blockDim.x)
+        a += part[i];
+    a = group_sum(a);
+    if (threadIdx.x == 0)
+        *sumsq = accumulate ? *sumsq + a : a;
+}
+
+struct ClipBatch {
+    const void* g[kNormSegs];
+    void* out[kNormSegs];
+    uint64_t n[kNormSegs];
+    uint32_t tile_end[kNormSegs];
+    uint32_t total;
+    float max_norm, eps;
+    const double* sumsq;
+    float* norm;
+};
+
+template <int T>
+__global__ __launch_bounds__(kBlockThreads) void clip_kernel(ClipBatch b) {
+    using G = NormGeom<T>;
+    const double norm = __builtin_sqrt(*b.sumsq);
+    if (b.norm && blockIdx.x == 0 && threadIdx.x == 0)
+        *b.norm = (float)norm;
+    const double q = (double)b.max_norm / (norm + (double)b.eps);
+    const float c = q >= 1.0 ? 1.0f : (float)q;  // a NaN stays one
+    const SegmentFinder<kNormSegs> find(b.tile_end, (uint32_t)kNormSegs);
+    const int lane = lane_id();
+    for (size_t ts = wave_id(); ts < b.total; ts += wave_count()) {
+        const uint32_t t = (uint32_t)ts, s = find(t);
+        const uint64_t base = (uint64_t)(t - (s ? b.tile_end[s - 1] : 0u)) * G::TILE;
+        const void* g = b.g[s];
+        void* out = b.out[s];
+        const uint64_t n = b.n[s];
+        if (c == 1.0f && out == g)
+            continue;
+        if (base + G::TILE <= n) {
+            u4 w[kNormU];
+#pragma unroll
+            for (int u = 0; u < kNormU; ++u) {
+                const uint64_t i0 = base + (uint64_t)u * G::SUB + (uint64_t)lane * G::VEC;
+                w[u] = ld_stream((const u4*)((const char*)g + i0 * (16 / G::VEC)));
+            }
+#pragma unroll
+            for (int u = 0; u < kNormU; ++u) {
+                const uint64_t i0 = base + (uint64_t)u * G::SUB + (uint64_t)lane * G::VEC;
+                float x[G::VEC];
+                widen<T>(w[u], x);
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (T == kF32)
+                        o[j] = fbits(c * x[j]);
+                    else
+                        o[j] = pack_products<T>(c * x[2 * j], c * x[2 * j + 1]);
+                }
+                st_stream(u4{o[0], o[1], o[2], o[3]}, (u4*)((char*)out + i0 * (16 / G::VEC)));
+            }
+        } else {
+            for (uint64_t i = base + lane; i < n; i += kWave) {
+                const float x = c * load1<T>(g, i);
+                if constexpr (T == kF32)
+                    ((float*)out)[i] = x;
+                else
+                    ((uint16_t*)out)[i] = (uint16_t)pack_products<T>(x, 0.0f);
+            }
+        }
+    }
+}
+
+template <int T>
+uint64_t tiles_of(uint64_t n) {
+    return (n + NormGeom<T>::TILE - 1) / NormGeom<T>::TILE;
+}
+
+void set_out(NormBatch&, uint32_t, void*) {}
+void set_out(ClipBatch& b, uint32_t k, void* out) { b.out[k] = out; }
+
+// Fills a launch's table from segs[i] on and returns the first segment that
+// the next launch takes.  The ABI layer holds a call to 2^41 elements, so the
+// tiles of a launch (1024 elements at least, one ragged one a segment) stay
+// below 2^32.
+template <int T, typename B>
+uint32_t fill(B& b, const GradSegment* segs, uint32_t i, uint32_t n_seg) {
+    uint64_t tiles = 0;
+    uint32_t k = 0;
+    for (; i < n_seg && k < (uint32_t)kNormSegs; ++i, ++k) {
+        b.g[k] = segs[i].g;
+        b.n[k] = segs[i].n;
+        set_out(b, k, segs[i].out);
+        tiles += tiles_of<T>(segs[i].n);
+        b.tile_end[k] = (uint32_t)tiles;
+    }
+    for (; k < (uint32_t)kNormSegs; ++k)
+        b.tile_end[k] = UINT32_MAX;
+    b.total = (uint32_t)tiles;
+    return i;
+}
+
+inline uint32_t norm_wgs(uint64_t tiles) {
+    return (uint32_t)std::min<uint64_t>((tiles + 3) / 4, kNormMaxWgs);
+}
+
+template <int T>
+hipError_t sumsq_t(const GradSegment* segs, uint32_t n_seg, uint32_t accumulate, double* sumsq,
+                   double* partials, hipStream_t st) {
+    uint64_t np = 0;
+    for (uint32_t i = 0; i < n_seg;) {
+        NormBatch b = {};
+        const uint32_t first = i;
+        i = fill<T>(b, segs, i, n_seg);
+        // Few tiles: one workgroup sums them and writes the result, one launch
+        // in place of two.
+        uint32_t last = first == 0 && i == n_seg && b.total <= kNormOneWg;
+        const uint32_t wgs = last ? 1 : norm_wgs(b.total);
+        double* out = last ? sumsq : partials + np;
+        void* args[] = {(void*)&b, (void*)&out, (void*)&last, (void*)&accumulate};
+        const hipError_t e = hipLaunchKernel((const void*)&sumsq_kernel<T>, dim3(wgs),
+                                             dim3(last ? 1024 : kBlockThreads), args, 0, st);
+        if (e != hipSuccess || last)
+            return e;
+        np += wgs;
+    }
+    void* args[] = {(void*)&partials, (void*)&np, (void*)&sumsq, (void*)&accumulate};
+    return hipLaunchKernel((const void*)&sumsq_join_kernel, dim3(1),
+                           dim3(np > 256 ? 1024 : 256), args, 0, st);
+}
+
+template <int T>
+hipError_t clip_t(const GradSegment* segs, uint32_t n_seg, const double* sumsq, float max_norm,
+                  float eps, float* norm, hipStream_t st) {
+    uint32_t i = 0;
+    do {  // at least one launch: it writes the norm
+        ClipBatch b = {};
+        b.max_norm = max_norm;
+        b.eps = eps;
+        b.sumsq = sumsq;
+        b.norm = i == 0 ? norm : nullptr;
+        i = fill<T>(b, segs, i, n_seg);
+        void* args[] = {(void*)&b};
+        const hipError_t e =
+            hipLaunchKernel((const void*)&clip_kernel<T>, dim3(std::max(norm_wgs(b.total), 1u)),
+                            dim3(kBlockThreads), args, 0, st);
+        if (e != hipSuccess)
+            return e;
+    } while (i < n_seg);
+    return hipSuccess;
+}
+
+}  // namespace
+
+// One partial for each workgroup of each launch.
+size_t grad_sumsq_workspace(uint32_t n_seg) {
+    const size_t launches = std::max<size_t>(1, (n_seg + (size_t)kNormSegs - 1) / kNormSegs);
+    return sizeof(double) * kNormMaxWgs * launches;
+}
+
+hipError_t launch_grad_sumsq(const GradSegment* segs, uint32_t n_seg, int g_type, bool accumulate,
+                             double* sumsq, double* partials, hipStream_t stream) {
+    switch (g_type) {
+        case kF32: return sumsq_t<kF32>(segs, n_seg, accumulate, sumsq, partials, stream);
+        case kBF16: return sumsq_t<kBF16>(segs, n_seg, accumulate, sumsq, partials, stream);
+        case kF16: return sumsq_t<kF16>(segs, n_seg, accumulate, sumsq, partials, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_grad_clip(const GradSegment* segs, uint32_t n_seg, int g_type,
+                            const double* sumsq, float max_norm, float eps, float* norm,
+                            hipStream_t stream) {
+    switch (g_type) {
+        case kF32: return clip_t<kF32>(segs, n_seg, sumsq, max_norm, eps, norm, stream);
+        case kBF16: return clip_t<kBF16>(segs, n_seg, sumsq, max_norm, eps, norm, stream);
+        case kF16: return clip_t<kF16>(segs, n_seg, sumsq, max_norm, eps, norm, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace zq

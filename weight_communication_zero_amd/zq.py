@@ -1,4 +1,4 @@
-"""ctypes binding of libzq (include/zq.h): argument marshalling only.
+"""ctypes binding of libzq (include/zq.h, include/zq_train.h): argument marshalling only.
 
 Every function takes torch tensors (device memory) or raw integer device
 pointers, converts them to the C ABI's plain pointers and sizes, passes the
@@ -21,6 +21,8 @@ LIB_PATH = os.environ.get("ZQ_LIB") or os.path.join(_HERE, "libzq.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "zq.h")
 
 ZQ_FP32, ZQ_BF16, ZQ_FP16 = 0, 1, 2
+ZQ_I32, ZQ_I64 = 0, 1
+ZQ_GRAD_WRITE, ZQ_GRAD_ADD, ZQ_GRAD_ADD_SR = 0, 1, 2
 
 STATUS = {
     0: "ZQ_OK", 1: "ZQ_ERR_NULL", 2: "ZQ_ERR_SIZE", 3: "ZQ_ERR_BLOCK", 4: "ZQ_ERR_ALIGN",
@@ -48,6 +50,11 @@ class DrSegment(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("codes_stride", C.c_uint64),
                 ("scales_stride", C.c_uint64), ("n", C.c_uint64), ("out", C.c_void_p),
                 ("rq_codes", C.c_void_p), ("rq_scales", C.c_void_p), ("rq_ef", C.c_void_p)]
+
+
+class GradSegment(C.Structure):
+    """zq_grad_segment of include/zq_train.h."""
+    _fields_ = [("g", C.c_void_p), ("out", C.c_void_p), ("n", C.c_uint64)]
 
 
 class ZQError(RuntimeError):
@@ -88,6 +95,19 @@ def _load() -> C.CDLL:
     L.zq_num_blocks.restype = sz
     L.zq_status_str.argtypes = [i32]
     L.zq_status_str.restype = C.c_char_p
+    L.zq_embed_lookup.argtypes = [vp, i32, u64, u64, vp, i32, sz, f32, vp, i32, vp]
+    L.zq_embed_lookup_int8.argtypes = [vp, vp, u32, u64, u64, vp, i32, sz, f32, vp, i32, vp]
+    L.zq_embed_grad.argtypes = [vp, i32, vp, i32, sz, u64, u64, f32, vp, i32, i32, u64, u64, vp, sz,
+                                vp]
+    L.zq_grad_sumsq_batched.argtypes = [vp, u32, i32, i32, vp, vp, sz, vp]
+    L.zq_grad_clip_batched.argtypes = [vp, u32, i32, vp, f32, f32, vp, vp]
+    for f in ("zq_embed_lookup", "zq_embed_lookup_int8", "zq_embed_grad", "zq_grad_sumsq_batched",
+              "zq_grad_clip_batched"):
+        getattr(L, f).restype = i32
+    L.zq_embed_grad_workspace.argtypes = [sz, u64, u64]
+    L.zq_embed_grad_workspace.restype = sz
+    L.zq_grad_sumsq_workspace.argtypes = [u32]
+    L.zq_grad_sumsq_workspace.restype = sz
     L.zq_abi_version.argtypes = []
     L.zq_abi_version.restype = u32
     return L
@@ -157,6 +177,8 @@ _BF16 = (torch.bfloat16,)
 _FLOAT = (torch.float32, torch.bfloat16, torch.float16)
 _U8 = (torch.uint8,)
 _I8 = (torch.int8,)
+_F64 = (torch.float64,)
+_INDEX = (torch.int32, torch.int64)
 
 
 def _check(fn: str, st: int) -> None:
@@ -367,3 +389,120 @@ def zq_dequant_reduce_batched(segments, P: int, block: int, alpha: float, rq_bet
     _check("zq_dequant_reduce_batched",
            lib.zq_dequant_reduce_batched(table.ptr, len(table.segments), P, block, alpha, rq_beta_e,
                                          rq_beta_r, _stream(stream)))
+
+
+def _index(t) -> int:
+    return ZQ_I64 if t.dtype == torch.int64 else ZQ_I32
+
+
+def _rows_dim(name: str, t) -> tuple[int, int]:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions [rows, dim], not {tuple(t.shape)}")
+    return t.shape[0], t.shape[1]
+
+
+def zq_embed_lookup(table, ids, scale: float, out, stream=None) -> None:
+    """out[t] = scale * table[ids[t]] (+0 where ids[t] is outside the table):
+    table [rows, dim] fp32/bf16/fp16, ids int32/int64 of any shape, out
+    fp32/bf16/fp16 with ids.numel() * dim elements."""
+    rows, dim = _rows_dim("table", table)
+    n = ids.numel()
+    _need("table", table, rows * dim, _FLOAT)
+    _need("ids", ids, n, _INDEX)
+    _need("out", out, n * dim, _FLOAT)
+    _check("zq_embed_lookup",
+           lib.zq_embed_lookup(_p(table), _dtype(table), rows, dim, _p(ids), _index(ids), n, scale,
+                               _p(out), _dtype(out), _stream(stream)))
+
+
+def zq_embed_lookup_int8(codes, scales, block: int, ids, scale: float, out, stream=None) -> None:
+    """zq_embed_lookup from a table in qwZ's form: codes [rows, dim] int8 and
+    scales fp32, as zq_quant_int8 writes them for the flat table."""
+    rows, dim = _rows_dim("codes", codes)
+    n = ids.numel()
+    _need("codes", codes, rows * dim, _I8)
+    _need("scales", scales, (rows * dim + block - 1) // block if block > 0 else 0, _F32)
+    _need("ids", ids, n, _INDEX)
+    _need("out", out, n * dim, _FLOAT)
+    _check("zq_embed_lookup_int8",
+           lib.zq_embed_lookup_int8(_p(codes), _p(scales), block, rows, dim, _p(ids), _index(ids),
+                                    n, scale, _p(out), _dtype(out), _stream(stream)))
+
+
+def embed_grad_workspace(n_tok: int, rows: int, dim: int) -> int:
+    """Bytes of workspace zq_embed_grad needs."""
+    return lib.zq_embed_grad_workspace(n_tok, rows, dim)
+
+
+def zq_embed_grad(dout, ids, scale: float, grad, mode: int, workspace, seed: int = 0,
+                  counter_base: int = 0, stream=None) -> None:
+    """The lookup's gradient by sorted tokens: grad [rows, dim] (fp32/bf16/fp16)
+    is written (ZQ_GRAD_WRITE), or added to with rounding to nearest
+    (ZQ_GRAD_ADD) or stochastic rounding (ZQ_GRAD_ADD_SR, bf16).  dout has
+    ids.numel() * dim elements; workspace is a uint8 tensor of at least
+    embed_grad_workspace(ids.numel(), rows, dim) bytes, one for each call that
+    may run at the same time."""
+    rows, dim = _rows_dim("grad", grad)
+    n = ids.numel()
+    _need("dout", dout, n * dim, _FLOAT)
+    _need("ids", ids, n, _INDEX)
+    _need("grad", grad, rows * dim, _FLOAT)
+    _need("workspace", workspace, embed_grad_workspace(n, rows, dim), _U8)
+    _check("zq_embed_grad",
+           lib.zq_embed_grad(_p(dout), _dtype(dout), _p(ids), _index(ids), n, rows, dim, scale,
+                             _p(grad), _dtype(grad), mode, seed, counter_base, _p(workspace),
+                             workspace.numel() if workspace is not None else 0, _stream(stream)))
+
+
+class GradSegmentTable:
+    """A marshalled segment table for zq_grad_sumsq_batched and
+    zq_grad_clip_batched: pairs (g, out) of gradient tensors of one dtype,
+    where out is g itself, another buffer of g's size, or None (only the sum of
+    squares is wanted).  Build it once for a fixed set of buffers."""
+
+    def __init__(self, segments):
+        self.segments = list(segments)
+        self.arr = (GradSegment * max(len(self.segments), 1))()
+        self.dtype = None
+        for i, (g, out) in enumerate(self.segments):
+            n = g.numel()
+            _need("g", g, n, _FLOAT)
+            if self.dtype is not None and _dtype(g) != self.dtype:
+                raise TypeError("all segments of a batch share one gradient dtype")
+            self.dtype = _dtype(g)
+            _need("out", out, n, (g.dtype,))
+            self.arr[i] = GradSegment(_p(g), _p(out), n)
+        self.ptr = C.cast(self.arr, C.c_void_p)
+
+
+def grad_sumsq_workspace(n_seg: int) -> int:
+    """Bytes of workspace zq_grad_sumsq_batched needs."""
+    return lib.zq_grad_sumsq_workspace(n_seg)
+
+
+def zq_grad_sumsq_batched(segments, sumsq, workspace, accumulate: bool = False,
+                          stream=None) -> None:
+    """sumsq (one float64) = [sumsq +] the sum of squares of every segment's g.
+    `segments`: a GradSegmentTable or an iterable of (g, out or None);
+    workspace: a uint8 tensor of grad_sumsq_workspace(n_seg) bytes."""
+    table = segments if isinstance(segments, GradSegmentTable) else GradSegmentTable(segments)
+    _need("sumsq", sumsq, 1, _F64)
+    _need("workspace", workspace, grad_sumsq_workspace(len(table.segments)), _U8)
+    _check("zq_grad_sumsq_batched",
+           lib.zq_grad_sumsq_batched(table.ptr, len(table.segments),
+                                     ZQ_FP32 if table.dtype is None else table.dtype,
+                                     1 if accumulate else 0, _p(sumsq), _p(workspace),
+                                     workspace.numel(), _stream(stream)))
+
+
+def zq_grad_clip_batched(segments, sumsq, max_norm: float, eps: float = 1e-6, norm=None,
+                         stream=None) -> None:
+    """out = g * min(1, max_norm / (sqrt(sumsq) + eps)) for every segment;
+    norm (one float32, optional) gets sqrt(sumsq)."""
+    table = segments if isinstance(segments, GradSegmentTable) else GradSegmentTable(segments)
+    _need("sumsq", sumsq, 1, _F64)
+    _need("norm", norm, 1, _F32)
+    _check("zq_grad_clip_batched",
+           lib.zq_grad_clip_batched(table.ptr, len(table.segments),
+                                    ZQ_FP32 if table.dtype is None else table.dtype, _p(sumsq),
+                                    max_norm, eps, _p(norm), _stream(stream)))
