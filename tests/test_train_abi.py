@@ -107,13 +107,16 @@ def test_embed_grad_refusals():
 def test_embed_grad_workspace():
     f = L.zq_embed_grad_workspace
     assert f(0, 10, 64) == 0 and f(5, 0, 64) == 0 and f(5, 10, 0) == 0 and f(2 ** 30 + 1, 10, 8) == 0
-    # Positions and keys, the row flags, and an eighth of an fp32 copy of dout
-    # for the long runs' partials.
-    last = 0
-    for n in (1, 64, 65, 8192, 8193, 32768, 10 ** 6):
-        b = f(n, 32000, 4096)
-        assert b >= last and 8 * n <= b < 16 * n + 32000 + 2 ** 20 + (n // 32 + 2) * 4096 * 4 + 4096
-        last = b
+    # Keys and positions, and at most an eighth of an fp32 copy of dout (an
+    # eighth only up to some 64 MB of it) for the partials of long runs.  A
+    # workspace made for some number of tokens serves every smaller number.
+    for dim in (1, 768, 4096, 2 ** 23):
+        last = 0
+        for n in sorted({1, 16, 17, 64, 65, 8192, 131072, 131073, 10 ** 6} | set(range(90, 140000, 997))):
+            b = f(n, 32000, dim)
+            assert last <= b
+            assert 8 * n <= b <= 17 * n + 2 ** 20 + max(n * dim // 8 + 8 * dim + 64, 2 ** 26)
+            last = b
     assert zq.embed_grad_workspace(100, 10, 64) == f(100, 10, 64)
 
 

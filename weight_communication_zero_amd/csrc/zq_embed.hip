@@ -4,9 +4,10 @@
 //
 // Pure data movement: it reads each named row (4 / 2 / 1 + 4/B bytes an
 // element) and writes 4 / 2 bytes an element.  The output is walked as one
-// flat run of 8-element groups, a lane per group, so any dim fills the waves;
-// a wave finds its first group's token by one scalar division and a lane its
-// own from there.
+// flat run of groups of G elements, a lane per group, so any dim fills the
+// waves; a wave finds its first group's token by one scalar division and a
+// lane its own from there.  G is 4 where an element has four bytes on either
+// side, so that every access covers whole lines, else 8.
 #include "zq_rows.h"
 
 namespace zq {
@@ -14,9 +15,15 @@ namespace {
 
 constexpr int kLookU = 4;  // groups a lane has in flight
 
+template <int IN, int OUT>
+constexpr int group_elems() {
+    return IN == kF32 || OUT == kF32 ? 4 : 8;
+}
+
 template <int IN, int OUT, bool WHOLE>
 __global__ __launch_bounds__(kBlockThreads) void lookup_kernel(LookupArgs a) {
-    const uint32_t per_row = (uint32_t)((a.dim + 7) / 8);
+    constexpr int G = group_elems<IN, OUT>();
+    const uint32_t per_row = (uint32_t)((a.dim + G - 1) / G);
     const uint64_t groups = a.n_tok * per_row;
     const uint32_t lane = (uint32_t)lane_id();
     for (uint64_t w = wave_id(); w * (kWave * kLookU) < groups; w += wave_count()) {
@@ -31,67 +38,53 @@ __global__ __launch_bounds__(kBlockThreads) void lookup_kernel(LookupArgs a) {
             const uint32_t r = r0 + u * kWave;
             const uint32_t q = r / per_row;
             tok[u] = t0 + q;
-            col[u] = (r - q * per_row) * 8;
+            col[u] = (r - q * per_row) * G;
             in[u] = g0 + (uint64_t)u * kWave + lane < groups;
-            row[u] = in[u] ? token_id(a.ids, a.id64, tok[u]) : UINT64_MAX;
-            there[u] = row[u] < a.rows;
+            // Loads without branches around them stay in flight together: past
+            // the end the last token is read, and row 0 for an id of no row.
+            const uint64_t id = token_id(a.ids, a.id64, min(tok[u], a.n_tok - 1));
+            there[u] = id < a.rows;
+            row[u] = there[u] ? id : 0;
         }
-        float x[kLookU][8];
+        Raw<IN, G> v[kLookU];
+        float s0[kLookU], s1[kLookU];
 #pragma unroll
         for (int u = 0; u < kLookU; ++u) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[u][j] = 0.0f;
-            if (!there[u])
-                continue;
             const uint64_t e = row[u] * a.dim + col[u];
             const uint32_t left = (uint32_t)a.dim - col[u];
+            v[u] = load_group<IN, G, WHOLE, false>(a.table, e, left);
             if constexpr (IN == kQ8) {
-                const int8_t* c = (const int8_t*)a.table + e;
-                uint32_t v[2] = {0, 0};
-                if (WHOLE) {
-                    const u2 k = *(const u2*)c;
-                    v[0] = k.x;
-                    v[1] = k.y;
-                } else if (left >= 8) {
-                    const u2 k = (u2) * (const u2a1*)c;
-                    v[0] = k.x;
-                    v[1] = k.y;
-                } else {
-#pragma unroll
-                    for (uint32_t j = 0; j < 7; ++j)
-                        if (j < left)
-                            v[j >> 2] |= (uint32_t)(uint8_t)c[j] << (8 * (j & 3));
-                }
-                // Eight elements touch two blocks at most (a block has 32 or more).
-                const uint64_t last = e + (left < 8 ? left : 8) - 1;
-                const float s0 = a.scales[e >> a.log2b];
-                const float s1 = WHOLE ? s0 : a.scales[last >> a.log2b];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float s = (WHOLE || (e + j) >> a.log2b == e >> a.log2b) ? s0 : s1;
-                    x[u][j] = (float)((int32_t)(v[j >> 2] << (24 - 8 * (j & 3))) >> 24) * s;
-                }
-            } else {
-                widen8<IN>(load8<IN, WHOLE>(a.table, e, left), x[u]);
+                // A group touches two blocks at most (a block has 32 elements or more).
+                s0[u] = a.scales[e >> a.log2b];
+                s1[u] = WHOLE ? s0[u] : a.scales[(e + (left < G ? left : G) - 1) >> a.log2b];
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[u][j] *= a.scale;
         }
 #pragma unroll
-        for (int u = 0; u < kLookU; ++u)
+        for (int u = 0; u < kLookU; ++u) {
+            float x[G];
+            widen<IN, G>(v[u], x);
+            if constexpr (IN == kQ8) {
+                const uint64_t e = row[u] * a.dim + col[u];
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    x[j] *= WHOLE || (e + j) >> a.log2b == e >> a.log2b ? s0[u] : s1[u];
+            }
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+                x[j] = there[u] ? a.scale * x[j] : 0.0f;
             if (in[u])
-                store8<OUT, WHOLE>(narrow8<OUT>(x[u]), a.out, tok[u] * a.dim + col[u],
-                                   (uint32_t)a.dim - col[u]);
+                store_group<OUT, G, WHOLE, true>(narrow<OUT, G>(x), a.out, tok[u] * a.dim + col[u],
+                                                 (uint32_t)a.dim - col[u]);
+        }
     }
 }
 
 template <int IN, int OUT>
 hipError_t lookup_t(const LookupArgs& a, hipStream_t st) {
+    constexpr int G = group_elems<IN, OUT>();
     const uint64_t per_wave = kWave * kLookU;
-    const uint64_t tiles = (a.n_tok * ((a.dim + 7) / 8) + per_wave - 1) / per_wave;
-    const void* fn = a.dim % 8 == 0 ? (const void*)&lookup_kernel<IN, OUT, true>
+    const uint64_t tiles = (a.n_tok * ((a.dim + G - 1) / G) + per_wave - 1) / per_wave;
+    const void* fn = a.dim % G == 0 ? (const void*)&lookup_kernel<IN, OUT, true>
                                     : (const void*)&lookup_kernel<IN, OUT, false>;
     void* args[] = {(void*)&a};
     return hipLaunchKernel(fn, grid_for_tiles(tiles, kGeomReduce), dim3(kGeomReduce.threads), args,

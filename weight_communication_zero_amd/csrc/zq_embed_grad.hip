@@ -2,22 +2,20 @@
 //   S[v, j] = sum over the tokens t with id v, ascending, of dout[t, j]
 //   G = fl(scale * S);  grad = rne(G) | rne(fl(grad + G)) | SR(fl(grad + G))
 //
-// 1. Sort.  The tokens' positions are sorted by row with a stable counting
-//    sort, least significant digit first, so a row's tokens keep ascending
-//    order; ids that name no row take the key `rows` and come last.  Up to
-//    kSmallTokens tokens one workgroup sorts in LDS in one launch; more are
-//    split over at most kSortBlocks workgroups, two launches a digit (count,
-//    scatter; every workgroup adds up the counts before it by itself).
-// 2. Sum.  The sorted positions are cut into chunks of kChunk.  A wave takes a
-//    chunk and 512 columns and sums the runs (equal rows) that begin in its
-//    chunk, up to the end of the next chunk, in registers, and writes a run
-//    that ends there to the table.  A longer run leaves fp32 partials: the
-//    wave it began in one, and each later chunk that it reaches one.  In the
-//    write mode the same launch clears the rows that no token names.
+// 1. Sort.  The tokens' positions are ordered by row, ascending within a row;
+//    ids that name no row take the key `rows` and come last.  One launch up to
+//    kRangeTokens tokens, two a digit beyond (below, at the kernels).
+// 2. Sum.  The sorted positions are cut into chunks.  A wave takes a chunk and
+//    512 columns and sums the runs (equal rows) that begin in its chunk, up to
+//    the end of the next chunk, in registers, and writes a run that ends there
+//    to the table.  A longer run leaves fp32 partials: the wave it began in
+//    one, and each later chunk that it reaches one.
 // 3. Join.  The partials of each long run are added in order and written.
+// The write mode clears the whole table in the sort's launches, whose few
+// workgroups leave the memory idle; the sums then overwrite the named rows.
 // Every row is written by one wave per column group, and the grouping depends
-// on the ids alone, so equal inputs give equal bits; integer atomics only
-// count.
+// on the ids and sizes alone, so equal inputs give equal bits; integer atomics
+// only count.
 #include <algorithm>
 
 #include "zq_rows.h"
@@ -26,28 +24,54 @@ namespace zq {
 namespace {
 
 constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr uint32_t kCols = kWave * 8;
+
+// Sort of up to kRangeTokens tokens and kRangeRows rows.
+constexpr uint64_t kRangeTokens = 1 << 16;
+constexpr uint64_t kRangeRows = 1 << 20;
+constexpr uint32_t kRangeBins = 512;  // most rows a workgroup takes
+constexpr uint32_t kRangeWgs = 64;
+constexpr uint32_t kRangeThreads = 1024;
+
+// Sort by digits.
 constexpr uint32_t kDigitBits = 9;
 constexpr uint32_t kBins = 1u << kDigitBits;
-constexpr uint32_t kSmallThreads = 1024;
-constexpr uint32_t kSmallTokens = 8192;
 constexpr uint32_t kSortThreads = 512;
 constexpr uint32_t kSortItems = 4;
 constexpr uint32_t kSortRound = kSortThreads * kSortItems;
 constexpr uint32_t kSortBlocks = 256;
-constexpr uint32_t kChunk = 32;
-constexpr uint32_t kCols = kWave * 8;
+
 constexpr uint32_t kJoinThreads = 512;
-constexpr uint64_t kClearBytes = 64 << 10;
+constexpr uint64_t kClearBytes = 64 << 10;  // a workgroup clears at a time
+constexpr uint64_t kClearWgs = 256;  // at most, each in a loop
+constexpr uint64_t kMaxWgs = 1 << 20;
+
+// Tokens of a chunk.  Short chunks give more waves, each with a shorter chain
+// of loads and stores; long ones leave fewer partials of long runs.
+constexpr uint64_t kWantWaves = 8192;
+uint32_t chunk_tokens(uint64_t n_tok, uint64_t col_tiles) {
+    for (uint32_t c = 32; c > 8; c /= 2)
+        if ((n_tok + c - 1) / c * col_tiles >= kWantWaves)
+            return c;
+    return 8;
+}
+
+bool sorts_by_range(uint64_t n_tok, uint64_t rows) {
+    return n_tok <= kRangeTokens && rows <= kRangeRows;
+}
 
 // How the caller's workspace is laid out; every part on a 256-byte boundary.
 struct Layout {
-    uint64_t key[2], pos[2];  // ping-pong buffers of the sort, u32 [n_tok]
-    uint64_t count;           // u32 [kSortBlocks][kBins]
-    uint64_t named;           // one byte per row: some token names it
-    uint64_t runs;            // u32 [1 + chunks]: number of long runs, first chunks
+    uint64_t key[2], pos[2];  // u32 [n_tok] each; the second pair for the sort by digits
+    uint64_t count;           // u32 [kSortBlocks][kBins], for the sort by digits
+    uint64_t runs;            // u32 [1 + chunks]: number of long runs, their first chunks
     uint64_t part;            // fp32 [chunks + 1][pitch]: partials of the long runs
-    uint64_t pitch, chunks, bytes;
+    uint64_t pitch, col_tiles, chunk, chunks, bytes;
 };
+
+uint64_t part_floats(uint64_t n_tok, uint64_t chunk, uint64_t pitch) {
+    return n_tok > 2 * chunk ? ((n_tok + chunk - 1) / chunk + 1) * pitch : 0;
+}
 
 Layout layout(uint64_t n_tok, uint64_t rows, uint64_t dim) {
     Layout l = {};
@@ -57,34 +81,60 @@ Layout layout(uint64_t n_tok, uint64_t rows, uint64_t dim) {
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-    l.chunks = (n_tok + kChunk - 1) / kChunk;
+    l.col_tiles = (dim + kCols - 1) / kCols;
+    l.chunk = chunk_tokens(n_tok, l.col_tiles);
+    l.chunks = (n_tok + l.chunk - 1) / l.chunk;
     l.pitch = (dim + 7) / 8 * 8;
-    const bool small = n_tok <= kSmallTokens;
-    for (int i = 0; i < 2; ++i) {
-        l.key[i] = small && i ? l.key[0] : take(4 * n_tok);
-        l.pos[i] = small && i ? l.pos[0] : take(4 * n_tok);
-    }
-    l.count = small ? at : take(4ull * kSortBlocks * kBins);
-    l.named = take(rows);
-    l.runs = take(4 * (1 + l.chunks));
-    l.part = take(n_tok > 2 * kChunk ? 4 * l.pitch * (l.chunks + 1) : 0);
+    l.key[0] = take(4 * n_tok);
+    l.pos[0] = take(4 * n_tok);
+    l.runs = take(4 * (2 + n_tok / 8));
+    const bool digits = !sorts_by_range(n_tok, rows);
+    l.key[1] = digits ? take(4 * n_tok) : 0;
+    l.pos[1] = digits ? take(4 * n_tok) : 0;
+    l.count = digits ? take(4ull * kSortBlocks * kBins) : 0;
+    // A workspace made for some number of tokens serves every smaller number:
+    // the most tokens that still take a shorter chunk may need more partials.
+    uint64_t part = part_floats(n_tok, l.chunk, l.pitch);
+    for (uint64_t c = 8; c < l.chunk; c *= 2)
+        part = std::max(part, part_floats((kWantWaves - 1) / l.col_tiles * 2 * c, c, l.pitch));
+    l.part = take(4 * part);
     l.bytes = at;
     return l;
+}
+
+// A share of the table for a launch to clear: 16-byte units [lo, hi) of p, and
+// the 2-byte units of the table's last, broken one.
+struct Clear {
+    char* p;
+    uint64_t lo, hi;
+    uint32_t tail;  // bytes after unit hi, in the last share
+};
+
+__device__ __forceinline__ void clear_share(const Clear& c, uint32_t wg, uint32_t wgs) {
+    constexpr uint64_t kUnits = kClearBytes / 16;
+    for (uint64_t u = c.lo + wg * kUnits; u < c.hi; u += wgs * kUnits) {
+        const uint64_t end = min(u + kUnits, c.hi);
+        for (uint64_t i = u + threadIdx.x; i < end; i += blockDim.x)
+            st_stream(u4{0, 0, 0, 0}, (u4*)c.p + i);
+    }
+    if (wg == 0 && 2 * threadIdx.x < c.tail)
+        *(uint16_t*)(c.p + c.hi * 16 + 2 * threadIdx.x) = 0;
 }
 
 struct SortArgs {
     const void* ids;
     uint32_t id64;
     uint32_t n, rows;
-    uint32_t per_block;  // tokens of a workgroup, a multiple of kSortRound
+    uint32_t wgs;        // workgroups of the sort; later ones clear
+    uint32_t per_wg;     // rows (range sort) or tokens (digits: a multiple of kSortRound)
     uint32_t shift, bits;
     const uint32_t* key_in;  // nullptr: the first digit, keys come from ids
     const uint32_t* pos_in;
     uint32_t* key_out;
     uint32_t* pos_out;
     uint32_t* count;
-    uint8_t* named;  // nullptr: not wanted
     uint32_t* runs;
+    Clear clear;
 };
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i) {
@@ -94,28 +144,28 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i) {
     return id < a.rows ? (uint32_t)id : a.rows;
 }
 
-// Lanes of the wave whose digit equals this lane's.
-__device__ __forceinline__ uint64_t same_digit(uint32_t d, uint32_t bits) {
-    uint64_t m = ~0ull;
+// Lanes of the wave, of those in `among`, whose digit equals this lane's.
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, uint32_t bits, uint64_t among) {
     for (uint32_t b = 0; b < bits; ++b) {
         const bool one = (d >> b) & 1;
         const uint64_t v = __builtin_amdgcn_ballot_w64(one);
-        m &= one ? v : ~v;
+        among &= one ? v : ~v;
     }
-    return m;
+    return among;
 }
 
-// Rank of this lane's item among the wave's items of the same digit so far,
-// counted in the wave's own row of LDS counters.  The wave's LDS accesses are
-// performed in order; the fences keep the compiler from reordering them.
-__device__ __forceinline__ uint32_t wave_rank(uint16_t* mine, uint32_t d, uint32_t bits) {
-    const uint64_t m = same_digit(d, bits);
-    const uint32_t below = (uint32_t)__builtin_popcountll(m & ((1ull << lane_id()) - 1));
-    const uint32_t base = mine[d];
+// Where this lane's item goes among the items of the same digit: the wave's
+// own LDS counter, plus the lanes before it in `same`; the counter moves on.
+// The wave's LDS accesses are performed in order; the fences keep the compiler
+// from reordering them.
+template <typename C>
+__device__ __forceinline__ uint32_t next_place(C* counter, uint64_t same, bool on) {
+    const uint32_t below = (uint32_t)__builtin_popcountll(same & ((1ull << lane_id()) - 1));
+    const uint32_t base = on ? *counter : 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (below == 0)
-        mine[d] = (uint16_t)(base + (uint32_t)__builtin_popcountll(m));
+    if (on && below == 0)
+        *counter = (C)(base + (uint32_t)__builtin_popcountll(same));
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     return base + below;
@@ -133,8 +183,8 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
     return v;
 }
 
-// Exclusive sum over the first kBins threads' values (a multiple of 64 of
-// them); called by the whole workgroup.
+// Exclusive sum over the values of the workgroup's first kBins threads;
+// called by the whole workgroup.
 __device__ __forceinline__ uint32_t bins_scan(uint32_t v, uint32_t* tmp) {
     const uint32_t t = threadIdx.x;
     const uint32_t inc = wave_scan(t < kBins ? v : 0);
@@ -142,99 +192,138 @@ __device__ __forceinline__ uint32_t bins_scan(uint32_t v, uint32_t* tmp) {
         tmp[t >> 6] = inc;
     __syncthreads();
     uint32_t before = 0;
+#pragma unroll
     for (uint32_t w = 0; w < kBins / kWave; ++w)
-        if (w < (t >> 6))
-            before += tmp[w];
+        before += w < (t >> 6) ? tmp[w] : 0;
     __syncthreads();
     return before + inc - v;
 }
 
-// One workgroup sorts up to kSmallTokens tokens: kItems a thread, in LDS.
-template <int kItems>
-__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortArgs a, uint32_t passes) {
-    constexpr uint32_t kWaves = kSmallThreads / kWave;
-    __shared__ uint16_t cnt[kWaves][kBins];
-    __shared__ uint32_t tmp[kBins / kWave];
-    __shared__ uint32_t key_s[kItems * kSmallThreads];
-    __shared__ uint16_t pos_s[kItems * kSmallThreads];
-    const uint32_t t = threadIdx.x, wave = t / kWave, lane = t % kWave;
-    const uint32_t first = wave * kWave * kItems + lane;
-    uint32_t key[kItems], pos[kItems], rank[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        pos[i] = first + i * kWave;
-        key[i] = pos[i] < a.n ? sort_key(a, pos[i]) : kNone;  // past the end: sorts last
+// Sort by ranges: workgroup w orders the tokens of rows [w, w + 1) * per_wg.
+// Every workgroup reads every id (from L2), so that nothing has to be exchanged
+// between workgroups and one launch does it all.  Each of its waves holds a
+// stretch of 64 K ids in registers and walks it twice.  The first walk counts
+// the range's rows, and the tokens of smaller keys, which go before the
+// workgroup's.  The second gathers the range's few tokens in an LDS ring, in
+// order, and places them 64 at a time.
+template <int K>
+__global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortArgs a) {
+    constexpr uint32_t kWaves = kRangeThreads / kWave;
+    constexpr int B = K < 8 ? K : 8;              // steps between looks at the ring
+    constexpr uint32_t kRing = 2 * kWave * B;     // holds 63 + 64 B entries
+    static_assert(kRangeBins == kBins, "bins_scan");
+    static_assert(kRangeBins * (uint64_t)K * kWave <= 1ull << 32, "a ring entry's two fields");
+    if (blockIdx.x >= a.wgs) {
+        clear_share(a.clear, blockIdx.x - a.wgs, gridDim.x - a.wgs);
+        return;
     }
-    if (a.named)
-        for (uint32_t r = t; r < a.rows; r += kSmallThreads)
-            a.named[r] = 0;
-    if (t == 0)
+    __shared__ uint32_t cnt[kWaves][kRangeBins];
+    __shared__ uint32_t ring_s[kWaves][kRing];
+    __shared__ uint32_t tmp[kRangeBins / kWave];
+    __shared__ uint32_t smaller[kWaves];
+    const uint32_t t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / kWave);
+    const uint32_t lane = t % kWave;
+    const uint32_t v0 = blockIdx.x * a.per_wg;
+    const uint32_t bins = min(a.per_wg, a.rows + 1 - v0);
+    const uint32_t lo = wave * (K * kWave);
+    uint32_t k[K];  // key - v0: below bins in the range; negative for smaller keys
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+        const uint32_t i = lo + u * kWave + lane;
+        k[u] = i < a.n ? sort_key(a, i) : kNone;
+    }
+    for (uint32_t i = t; i < kWaves * kRangeBins; i += kRangeThreads)
+        (&cnt[0][0])[i] = 0;
+    if (blockIdx.x == 0 && t == 0)
         a.runs[0] = 0;
-    const uint32_t mask = (1u << a.bits) - 1;
-    for (uint32_t p = 0; p < passes; ++p) {
-        const uint32_t shift = p * a.bits;
-        for (uint32_t i = t; i < kWaves * kBins; i += kSmallThreads)
-            (&cnt[0][0])[i] = 0;
-        __syncthreads();
+    __syncthreads();
+    uint32_t less = 0;
 #pragma unroll
-        for (int i = 0; i < kItems; ++i)
-            rank[i] = wave_rank(cnt[wave], (key[i] >> shift) & mask, a.bits);
-        __syncthreads();
-        uint32_t sum = 0;
-        if (t < kBins)
-            for (uint32_t w = 0; w < kWaves; ++w)
-                sum += cnt[w][t];
-        uint32_t at = bins_scan(sum, tmp);
-        if (t < kBins)
-            for (uint32_t w = 0; w < kWaves; ++w) {
-                const uint32_t c = cnt[w][t];
-                cnt[w][t] = (uint16_t)at;
-                at += c;
+    for (int u = 0; u < K; ++u) {
+        less += k[u] < v0;
+        k[u] -= v0;
+        if (k[u] < bins)
+            atomicAdd(&cnt[wave][k[u]], 1u);
+    }
+    less = wave_scan(less);
+    if (lane == kWave - 1)
+        smaller[wave] = less;
+    __syncthreads();
+    uint32_t sum = 0;
+    if (t < kRangeBins) {
+#pragma unroll
+        for (uint32_t w = 0; w < kWaves; ++w)
+            sum += cnt[w][t];
+    }
+    uint32_t at = bins_scan(sum, tmp);
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w)
+        at += smaller[w];
+    if (t < kRangeBins) {
+#pragma unroll
+        for (uint32_t w = 0; w < kWaves; ++w) {
+            const uint32_t c = cnt[w][t];
+            cnt[w][t] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    uint32_t bits = 0;
+    while ((bins - 1) >> bits)
+        ++bits;
+    // The wave's own ring: its LDS accesses are performed in order.
+    uint32_t* ring = ring_s[wave];
+    uint32_t put = 0, got = 0;
+    const auto place = [&](uint32_t n) {  // the ring's next n <= 64 entries
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const bool in = lane < n;
+        const uint32_t e = in ? ring[(got + lane) % kRing] : 0;
+        const uint32_t bin = e % kRangeBins;
+        const uint64_t same = same_digit(bin, bits, __builtin_amdgcn_ballot_w64(in));
+        const uint32_t to = next_place(&cnt[wave][bin], same, in);
+        if (in) {
+            a.key_out[to] = bin + v0;
+            a.pos_out[to] = lo + e / kRangeBins;
+        }
+        got += n;
+    };
+#pragma unroll
+    for (int u = 0; u < K; u += B) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const bool in = k[u + b] < bins;
+            const uint64_t any = __builtin_amdgcn_ballot_w64(in);
+            if (any) {
+                const uint32_t before = (uint32_t)__builtin_popcountll(any & ((1ull << lane) - 1));
+                if (in)
+                    ring[(put + before) % kRing] = k[u + b] + ((u + b) * kWave + lane) * kRangeBins;
+                put += (uint32_t)__builtin_popcountll(any);
             }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const uint32_t to = cnt[wave][(key[i] >> shift) & mask] + rank[i];
-            key_s[to] = key[i];
-            pos_s[to] = (uint16_t)pos[i];
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            key[i] = key_s[first + i * kWave];
-            pos[i] = pos_s[first + i * kWave];
-        }
+        while (put - got >= kWave)
+            place(kWave);
     }
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const uint32_t o = first + i * kWave;
-        if (o < a.n) {
-            a.key_out[o] = key[i];
-            a.pos_out[o] = pos[i];
-            if (a.named && key[i] < a.rows)
-                a.named[key[i]] = 1;  // after the clearing: barriers lie between
-        }
-    }
+    if (put != got)
+        place(put - got);
 }
 
-// Counts one digit of a workgroup's tokens.  The first digit's launch also
-// clears the row flags and the number of long runs.
+// Sort by digits: a stable counting sort, least significant digit first, over
+// at most kSortBlocks workgroups.  Counts one digit of a workgroup's tokens.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+    if (blockIdx.x >= a.wgs) {
+        clear_share(a.clear, blockIdx.x - a.wgs, gridDim.x - a.wgs);
+        return;
+    }
     __shared__ uint32_t cnt[kBins];
     const uint32_t t = threadIdx.x;
     for (uint32_t i = t; i < kBins; i += kSortThreads)
         cnt[i] = 0;
-    if (!a.key_in) {
-        if (a.named)
-            for (uint64_t r = (uint64_t)blockIdx.x * kSortThreads + t; r < a.rows;
-                 r += (uint64_t)gridDim.x * kSortThreads)
-                a.named[r] = 0;
-        if (blockIdx.x == 0 && t == 0)
-            a.runs[0] = 0;
-    }
+    if (!a.key_in && blockIdx.x == 0 && t == 0)
+        a.runs[0] = 0;
     __syncthreads();
-    const uint64_t lo = (uint64_t)blockIdx.x * a.per_block;
-    const uint64_t hi = min(lo + a.per_block, (uint64_t)a.n);
+    const uint64_t lo = (uint64_t)blockIdx.x * a.per_wg;
+    const uint64_t hi = min(lo + a.per_wg, (uint64_t)a.n);
     const uint32_t mask = (1u << a.bits) - 1;
     for (uint64_t i = lo + t; i < hi; i += kSortThreads)
         atomicAdd(&cnt[(sort_key(a, (uint32_t)i) >> a.shift) & mask], 1u);
@@ -245,6 +334,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
 
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) {
     static_assert(kSortThreads == kBins, "a thread per digit value");
+    if (blockIdx.x >= a.wgs) {
+        clear_share(a.clear, blockIdx.x - a.wgs, gridDim.x - a.wgs);
+        return;
+    }
     constexpr uint32_t kWaves = kSortThreads / kWave;
     __shared__ uint16_t cnt[kWaves][kBins];
     __shared__ uint32_t base[kBins];
@@ -253,14 +346,15 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) 
     // Where this workgroup's first token of digit value t goes: all tokens of
     // smaller digits, then those of this digit in earlier workgroups.
     uint32_t total = 0, earlier = 0;
-    for (uint32_t b = 0; b < gridDim.x; ++b) {
+#pragma unroll 8
+    for (uint32_t b = 0; b < a.wgs; ++b) {
         const uint32_t c = a.count[b * kBins + t];
         total += c;
         earlier += b < blockIdx.x ? c : 0;
     }
     base[t] = bins_scan(total, tmp) + earlier;
-    const uint64_t lo = (uint64_t)blockIdx.x * a.per_block;
-    const uint64_t hi = min(lo + a.per_block, (uint64_t)a.n);
+    const uint64_t lo = (uint64_t)blockIdx.x * a.per_wg;
+    const uint64_t hi = min(lo + a.per_wg, (uint64_t)a.n);
     const uint32_t mask = (1u << a.bits) - 1;
     for (uint64_t r = lo; r < hi; r += kSortRound) {
         for (uint32_t i = t; i < kWaves * kBins; i += kSortThreads)
@@ -272,11 +366,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) 
             const uint64_t at = r + wave * kWave * kSortItems + i * kWave + lane;
             key[i] = at < hi ? sort_key(a, (uint32_t)at) : kNone;
             pos[i] = at < hi ? (a.pos_in ? a.pos_in[at] : (uint32_t)at) : 0;
-            // Past the end: ranked last, and not written.
-            rank[i] = wave_rank(cnt[wave], (key[i] >> a.shift) & mask, a.bits);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kSortItems; ++i) {
+            // Past the end: all bits set, ranked last, and not written.
+            const uint32_t d = (key[i] >> a.shift) & mask;
+            rank[i] = next_place(&cnt[wave][d], same_digit(d, a.bits, ~0ull), true);
         }
         __syncthreads();
         uint32_t sum = 0;
+#pragma unroll
         for (uint32_t w = 0; w < kWaves; ++w) {
             const uint32_t c = cnt[w][t];
             cnt[w][t] = (uint16_t)sum;
@@ -292,8 +391,6 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) 
             const uint32_t to = base[d] + cnt[wave][d] + rank[i];
             a.key_out[to] = key[i];
             a.pos_out[to] = pos[i];
-            if (a.named && key[i] < a.rows)
-                a.named[key[i]] = 1;
         }
         __syncthreads();
         base[t] += sum;  // the pads counted in it belong to the last round only
@@ -303,19 +400,17 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) 
 struct SumArgs {
     const uint32_t* key;
     const uint32_t* pos;
-    const uint8_t* named;
     uint32_t* runs;
     float* part;
     uint64_t pitch;
-    uint32_t n, chunks, rows;
+    uint32_t n, rows;
+    uint32_t chunk, chunks;  // tokens of a chunk (8, 16 or 32), number of chunks
     uint32_t col_tiles;
     uint64_t dim;
     const void* dout;
     void* grad;
     float scale;
     uint64_t seed, cbase;
-    uint32_t sum_wgs;    // the workgroups after these clear rows
-    uint32_t clear_rows; // rows a workgroup clears at a time
 };
 
 // The eight 16-bit random numbers of indices q .. q + 7 (the layout of
@@ -354,138 +449,204 @@ __device__ __forceinline__ void random8(uint64_t q, uint64_t seed, uint32_t r[8]
         r[j] = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
 }
 
-// Writes a row's eight sums at element e = row * dim + col, of which `left`
-// exist; `old` are the buffer's values there (add modes).
+// The eight columns of a lane in its wave's group of kCols: eight consecutive
+// ones, or with an fp32 gradient two fours, kCols / 2 apart, so that each
+// access covers whole lines.
+template <int OUT>
+struct Cols {
+    static constexpr bool kSplit = OUT == kF32;
+    static constexpr int H = kSplit ? 2 : 1, G = 8 / H;
+    uint32_t col[H], left[H];  // first column, columns from there to the row's end
+    bool on[H];                // there is one (else the lane reads column 0, and writes nothing)
+
+    __device__ __forceinline__ Cols(uint32_t tile, uint32_t dim) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            col[h] = tile * kCols + h * (kCols / 2) + (uint32_t)lane_id() * G;
+            on[h] = col[h] < dim;
+            if (!on[h])
+                col[h] = 0;
+            left[h] = dim - col[h];
+        }
+    }
+};
+
+// A lane's columns of one row of an array of type T.
+template <int T, int OUT>
+struct RowBits {
+    Raw<T, Cols<OUT>::G> h[Cols<OUT>::H];
+};
+
+template <int T, int OUT, bool WHOLE, bool NT>
+__device__ __forceinline__ RowBits<T, OUT> load_row(const void* __restrict__ p, uint64_t row,
+                                                    uint64_t dim, const Cols<OUT>& c) {
+    RowBits<T, OUT> r;
+#pragma unroll
+    for (int h = 0; h < Cols<OUT>::H; ++h)
+        r.h[h] = load_group<T, Cols<OUT>::G, WHOLE, NT>(p, row * dim + c.col[h], c.left[h]);
+    return r;
+}
+
+template <int T, int OUT>
+__device__ __forceinline__ void widen_row(const RowBits<T, OUT>& r, float x[8]) {
+#pragma unroll
+    for (int h = 0; h < Cols<OUT>::H; ++h)
+        widen<T, Cols<OUT>::G>(r.h[h], x + h * Cols<OUT>::G);
+}
+
+// A long run's partial sums.
+template <int OUT>
+__device__ __forceinline__ void store_part(const float s[8], float* p, const Cols<OUT>& c) {
+#pragma unroll
+    for (int h = 0; h < Cols<OUT>::H; ++h)
+        if (c.on[h])
+#pragma unroll
+            for (int i = 0; i < Cols<OUT>::G; i += 4) {
+                const float* q = s + h * Cols<OUT>::G + i;
+                *(f4*)(p + c.col[h] + i) = f4{q[0], q[1], q[2], q[3]};
+            }
+}
+
+// dout is read nontemporally where an access covers whole lines (see zq_rows.h).
+// The gradient's rows are read and written plainly: 32768 tokens x 4096 added
+// into fp32 took 171.8 us with nontemporal reads of them, 168.5 with plain ones;
+// written (16384 x 2048) 81.4 us with nontemporal stores, 79.4 with plain ones.
+template <int IN, int OUT>
+constexpr bool dout_nt() {
+    return IN != kF32 || OUT == kF32;
+}
+
+// Writes a row's eight sums; `old` are the buffer's values there (add modes).
 template <int OUT, int MODE, bool WHOLE>
-__device__ __forceinline__ void finish(const SumArgs& a, const float s[8], const Raw8<OUT>& old,
-                                       uint64_t e, uint32_t left) {
+__device__ __forceinline__ void finish(const SumArgs& a, const float s[8],
+                                       const RowBits<OUT, OUT>& old, uint64_t row,
+                                       const Cols<OUT>& c) {
+    constexpr int H = Cols<OUT>::H, G = Cols<OUT>::G;
     float g[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         g[j] = a.scale * s[j];
     if constexpr (MODE != kGradWrite) {
         float o[8];
-        widen8<OUT>(old, o);
+        widen_row<OUT, OUT>(old, o);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             g[j] = o[j] + g[j];
     }
-    if constexpr (MODE == kGradAddSr) {
-        uint32_t r[8];
-        random8(a.cbase + e, a.seed, r);
-        Raw8<OUT> w;
-        uint32_t h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            h[j] = sr_bf16(g[2 * j], r[2 * j]) | (sr_bf16(g[2 * j + 1], r[2 * j + 1]) << 16);
-        w.w[0] = u4{h[0], h[1], h[2], h[3]};
-        store8<OUT, WHOLE>(w, a.grad, e, left);
-    } else {
-        store8<OUT, WHOLE>(narrow8<OUT>(g), a.grad, e, left);
+    for (int h = 0; h < H; ++h) {
+        const uint64_t e = row * a.dim + c.col[h];
+        Raw<OUT, G> r;
+        if constexpr (MODE == kGradAddSr) {
+            uint32_t r16[8];
+            random8(a.cbase + e, a.seed, r16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r.w[j] = sr_bf16(g[2 * j], r16[2 * j]) | (sr_bf16(g[2 * j + 1], r16[2 * j + 1]) << 16);
+        } else {
+            r = narrow<OUT, G>(g + h * G);
+        }
+        if (c.on[h])
+            store_group<OUT, G, WHOLE, false>(r, a.grad, e, c.left[h]);
     }
 }
 
-constexpr int kSumU = 4;  // tokens a wave has in flight
-
-// Sums positions [p, e) of the wave's window, one run after the other, each
-// run's sum going to `done(last position, sums)`.  ends has a bit at each
-// run's last position.
+// A wave's window of the sorted tokens: lane l holds the l-th from its chunk's
+// first on, two chunks of them.
 template <int IN, int OUT, int MODE, bool WHOLE>
-struct Walker {
+struct Window {
+    static constexpr int U = 8;  // tokens in flight
     const SumArgs& a;
-    uint32_t key, pos;  // lane l: the window's l-th sorted token
-    uint32_t col, left;
-    bool on;            // the lane has columns
+    uint32_t key, pos;
+    Cols<OUT> cols;
 
     __device__ __forceinline__ uint32_t key_at(uint32_t p) const {
         return __builtin_amdgcn_readlane(key, p);
     }
 
-    __device__ __forceinline__ void run(uint32_t p, uint32_t e, uint64_t ends, float* long_part,
+    // Sums positions [p, e), p < e, one run after the other; `ends` has a bit at
+    // each run's last position.  A run that ends at long_end goes to long_part,
+    // the others to the table.
+    __device__ __forceinline__ void sum(uint32_t p, uint32_t e, uint64_t ends, float* long_part,
                                         uint32_t long_end) const {
         float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        while (p < e) {
-            Raw8<IN> x[kSumU];
-            Raw8<OUT> old[kSumU];
+        for (; p < e; p += U) {
+            RowBits<IN, OUT> x[U];
+            RowBits<OUT, OUT> old[U];
 #pragma unroll
-            for (int u = 0; u < kSumU; ++u) {
-                if (p + u >= e)
-                    continue;
-                const uint64_t t = __builtin_amdgcn_readlane(pos, p + u);
-                if (on)
-                    x[u] = load8<IN, WHOLE>(a.dout, t * a.dim + col, left);
+            for (int u = 0; u < U; ++u) {
+                const uint32_t q = min(p + u, e - 1);  // past the end: read, not used
+                const uint64_t t = __builtin_amdgcn_readlane(pos, q);
+                x[u] = load_row<IN, OUT, WHOLE, dout_nt<IN, OUT>()>(a.dout, t, a.dim, cols);
                 if constexpr (MODE != kGradWrite)
-                    if (on && ((ends >> (p + u)) & 1) && p + u != long_end)
-                        old[u] = load8<OUT, WHOLE>(a.grad, (uint64_t)key_at(p + u) * a.dim + col,
-                                                   left);
+                    if (((ends >> q) & 1) && q != long_end)
+                        old[u] = load_row<OUT, OUT, WHOLE, false>(a.grad, key_at(q),
+                                                                                a.dim, cols);
             }
 #pragma unroll
-            for (int u = 0; u < kSumU; ++u) {
+            for (int u = 0; u < U; ++u) {
                 if (p + u >= e)
-                    continue;
+                    break;
                 float v[8];
-                widen8<IN>(x[u], v);
+                widen_row<IN, OUT>(x[u], v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     s[j] += v[j];
-                if ((ends >> (p + u)) & 1) {
-                    if (on) {
-                        if (p + u == long_end) {
-                            *(f4*)(long_part + col) = f4{s[0], s[1], s[2], s[3]};
-                            *(f4*)(long_part + col + 4) = f4{s[4], s[5], s[6], s[7]};
-                        } else {
-                            finish<OUT, MODE, WHOLE>(
-                                a, s, old[u], (uint64_t)key_at(p + u) * a.dim + col, left);
-                        }
-                    }
+                if (!((ends >> (p + u)) & 1))
+                    continue;
+                if (p + u == long_end)
+                    store_part<OUT>(s, long_part, cols);
+                else
+                    finish<OUT, MODE, WHOLE>(a, s, old[u], key_at(p + u), cols);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        s[j] = 0.0f;
-                }
+                for (int j = 0; j < 8; ++j)
+                    s[j] = 0.0f;
             }
-            p += kSumU;
         }
     }
 };
 
 template <int IN, int OUT, int MODE, bool WHOLE>
 __device__ __forceinline__ void sum_chunk(const SumArgs& a, uint32_t k, uint32_t tile) {
-    static_assert(2 * kChunk == kWave, "a chunk and its successor fill the lanes");
     const uint32_t lane = (uint32_t)lane_id();
-    const uint32_t i0 = k * kChunk;
-    const uint32_t i = i0 + lane;
-    Walker<IN, OUT, MODE, WHOLE> w = {a, kNone, 0, tile * kCols + lane * 8, 0, false};
-    w.on = w.col < a.dim;
-    w.left = w.on ? (uint32_t)a.dim - w.col : 0;
-    if (i < a.n) {
-        w.key = a.key[i];
-        w.pos = a.pos[i];
+    const uint32_t c = a.chunk, span = 2 * c;  // span <= 64
+    const uint32_t i0 = k * c;
+    Window<IN, OUT, MODE, WHOLE> w = {a, kNone, 0, Cols<OUT>(tile, (uint32_t)a.dim)};
+    if (lane < span && i0 + lane < a.n) {
+        w.key = a.key[i0 + lane];
+        w.pos = a.pos[i0 + lane];
     }
+    // The neighbours that decide how runs cross the window's borders, read at
+    // once with it: the tokens before this chunk and before the previous one,
+    // and the first one after the window.
+    const uint32_t before = k > 0 ? a.key[i0 - 1] : kNone;
+    const uint32_t before2 = k > 1 ? a.key[i0 - c - 1] : kNone;
+    const uint32_t after = i0 + span < a.n ? a.key[i0 + span] : kNone;
     const uint32_t first = w.key_at(0);
     if (first >= a.rows)
         return;  // ids that name no row, to the end
-    const bool cont = k > 0 && a.key[i0 - 1] == first;
-    // Bit p: a run starts at position p (the first kNone is one too).
-    uint32_t prev = __shfl_up(w.key, 1);
-    const uint64_t starts =
-        __builtin_amdgcn_ballot_w64(lane == 0 ? !cont : w.key != prev);
+    const bool cont = before == first;
+    // Bit p: a run starts at position p.  Lanes without a token hold kNone, the
+    // first of them is a start too.
+    const uint32_t prev = __shfl_up(w.key, 1);
+    const uint64_t starts = __builtin_amdgcn_ballot_w64(lane == 0 ? !cont : w.key != prev);
     const uint64_t ends = starts >> 1;
-    const uint32_t own = (uint32_t)(starts & ((1ull << kChunk) - 1));
-    uint32_t p = own ? (uint32_t)__builtin_ctz(own) : kChunk;
-    if (cont && k > 1 && a.key[i0 - kChunk - 1] == first) {
+    const uint32_t own = (uint32_t)(starts & ((1ull << c) - 1));
+    const uint32_t p = own ? (uint32_t)__builtin_ctz(own) : c;
+    if (cont && before2 == first) {
         // The run began before the previous chunk: this chunk's part of it.
         const uint32_t here = min(p, a.n - i0);
-        w.run(0, here, 1ull << (here - 1), a.part + (uint64_t)k * a.pitch, here - 1);
+        w.sum(0, here, 1ull << (here - 1), a.part + (uint64_t)k * a.pitch, here - 1);
     }
     if (!own)
         return;
     // The runs that start here; the last one may reach into the next chunk.
-    const uint64_t later = starts >> kChunk;
-    uint32_t e = later ? kChunk + (uint32_t)__builtin_ctzll(later) : kWave;
+    const uint64_t later = starts >> c;
+    uint32_t e = later ? min(c + (uint32_t)__builtin_ctzll(later), span) : span;
     uint32_t long_end = kNone;
-    if (e == kWave && i0 + kWave < a.n && a.key[i0 + kWave] == w.key_at(kWave - 1) &&
-        w.key_at(kWave - 1) < a.rows) {
-        long_end = kWave - 1;
+    const uint32_t last = w.key_at(span - 1);
+    if (e == span && last < a.rows && after == last) {
+        long_end = span - 1;
         if (tile == 0 && lane == 0)
             a.runs[1 + atomicAdd(&a.runs[0], 1u)] = k;
     }
@@ -493,37 +654,16 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& a, uint32_t k, uint32_t
     const uint64_t bad = __builtin_amdgcn_ballot_w64(w.key >= a.rows);
     if (bad)
         e = min(e, (uint32_t)__builtin_ctzll(bad));
-    w.run(p, e, ends | (1ull << (kWave - 1)), a.part + (uint64_t)(k + 1) * a.pitch, long_end);
-}
-
-template <int OUT, bool WHOLE>
-__device__ __forceinline__ void clear_rows(const SumArgs& a, uint32_t job) {
-    const uint64_t r0 = (uint64_t)job * a.clear_rows;
-    const uint32_t nr = (uint32_t)min((uint64_t)a.clear_rows, a.rows - r0);
-    const Raw8<OUT> zero = {};
-    const uint32_t per_row = (uint32_t)((a.dim + 7) / 8);
-    for (uint32_t r = 0; r < nr; ++r) {
-        if (a.named[r0 + r])
-            continue;
-        for (uint32_t g = threadIdx.x; g < per_row; g += kBlockThreads)
-            store8<OUT, WHOLE>(zero, a.grad, (r0 + r) * a.dim + (uint64_t)g * 8,
-                               (uint32_t)a.dim - g * 8);
-    }
+    if (p < e)
+        w.sum(p, e, ends | (1ull << (span - 1)), a.part + (uint64_t)(k + 1) * a.pitch, long_end);
 }
 
 template <int IN, int OUT, int MODE, bool WHOLE>
 __global__ __launch_bounds__(kBlockThreads) void sum_kernel(SumArgs a) {
-    if (MODE != kGradWrite || blockIdx.x < a.sum_wgs) {
-        const uint64_t jobs = (uint64_t)a.chunks * a.col_tiles;
-        const uint64_t waves = (uint64_t)a.sum_wgs * (kBlockThreads / kWave);
-        for (uint64_t j = wave_id(); j < jobs; j += waves) {
-            const uint32_t k = (uint32_t)(j / a.col_tiles);
-            sum_chunk<IN, OUT, MODE, WHOLE>(a, k, (uint32_t)(j - (uint64_t)k * a.col_tiles));
-        }
-    } else {
-        const uint32_t jobs = (uint32_t)(((uint64_t)a.rows + a.clear_rows - 1) / a.clear_rows);
-        for (uint32_t j = blockIdx.x - a.sum_wgs; j < jobs; j += gridDim.x - a.sum_wgs)
-            clear_rows<OUT, WHOLE>(a, j);
+    const uint64_t jobs = (uint64_t)a.chunks * a.col_tiles;
+    for (uint64_t j = wave_id(); j < jobs; j += wave_count()) {
+        const uint32_t k = (uint32_t)(j / a.col_tiles);
+        sum_chunk<IN, OUT, MODE, WHOLE>(a, k, (uint32_t)(j - (uint64_t)k * a.col_tiles));
     }
 }
 
@@ -534,20 +674,21 @@ __global__ __launch_bounds__(kBlockThreads) void sum_kernel(SumArgs a) {
 template <int OUT, int MODE, bool WHOLE>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(SumArgs a) {
     constexpr uint32_t kWaves = kJoinThreads / kWave;
+    constexpr int G = Cols<OUT>::G;
     __shared__ float part[kWaves][kCols];
     const uint32_t wave = threadIdx.x / kWave, lane = (uint32_t)lane_id();
     const uint64_t jobs = (uint64_t)a.runs[0] * a.col_tiles;
     for (uint64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
         const uint32_t k = a.runs[1 + j / a.col_tiles];
         const uint32_t tile = (uint32_t)(j % a.col_tiles);
-        const uint32_t row = a.key[(k + 2) * kChunk];
+        const uint32_t row = a.key[(k + 2) * a.chunk];
         // The chunks from k + 2 on that begin with the row: the first one
         // does, and the keys are sorted, so 64 probes narrow the end down.
         uint32_t lo = k + 2, hi = a.chunks;  // lo begins with the row; hi does not, or is the end
         while (hi - lo > 1) {
             const uint32_t step = (hi - lo + kWave - 1) / kWave;
             const uint64_t at = (uint64_t)lo + (uint64_t)lane * step;
-            const bool yes = at < hi && a.key[at * kChunk] == row;
+            const bool yes = at < hi && a.key[at * a.chunk] == row;
             const uint32_t c = (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(yes));
             hi = (uint32_t)min((uint64_t)hi, (uint64_t)lo + (uint64_t)c * step);
             lo += (c - 1) * step;
@@ -555,66 +696,75 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(SumArgs a) {
         const uint32_t slots = hi - (k + 1);
         const uint32_t s0 = k + 1 + (uint32_t)((uint64_t)slots * wave / kWaves);
         const uint32_t s1 = k + 1 + (uint32_t)((uint64_t)slots * (wave + 1) / kWaves);
-        const uint32_t col = tile * kCols + lane * 8;
-        const bool on = col < a.dim;
+        const Cols<OUT> c(tile, (uint32_t)a.dim);
         float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (on) {
 #pragma unroll 4
-            for (uint32_t i = s0; i < s1; ++i) {
-                const f4* q = (const f4*)(a.part + (uint64_t)i * a.pitch + col);
-                const f4 x = q[0], y = q[1];
+        for (uint32_t i = s0; i < s1; ++i) {
+            const float* q = a.part + (uint64_t)i * a.pitch;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[e] += x[e];
-                    s[4 + e] += y[e];
-                }
+            for (int g = 0; g < 8; g += 4) {
+                const f4 x = *(const f4*)(q + c.col[g / G] + g % G);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[g + e] += x[e];
             }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             part[wave][e * kWave + lane] = s[e];
         __syncthreads();
-        if (wave == 0 && on) {
+        if (wave == 0) {
             for (uint32_t w = 1; w < kWaves; ++w)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     s[e] += part[w][e * kWave + lane];
-            const uint64_t at = (uint64_t)row * a.dim + col;
-            const uint32_t left = (uint32_t)a.dim - col;
-            Raw8<OUT> old = {};
+            RowBits<OUT, OUT> old = {};
             if constexpr (MODE != kGradWrite)
-                old = load8<OUT, WHOLE>(a.grad, at, left);
-            finish<OUT, MODE, WHOLE>(a, s, old, at, left);
+                old = load_row<OUT, OUT, WHOLE, false>(a.grad, row, a.dim, c);
+            finish<OUT, MODE, WHOLE>(a, s, old, row, c);
         }
         __syncthreads();
     }
 }
 
 // ZQ_GRAD_WRITE without tokens.
-__global__ __launch_bounds__(kBlockThreads) void clear_kernel(char* p, uint64_t bytes) {
-    const uint64_t n16 = bytes / 16, step = (uint64_t)gridDim.x * kBlockThreads;
-    for (uint64_t i = (uint64_t)blockIdx.x * kBlockThreads + threadIdx.x; i < n16; i += step)
-        st_stream(u4{0, 0, 0, 0}, (u4*)p + i);
-    const uint64_t at = n16 * 16 + 2 * threadIdx.x;
-    if (blockIdx.x == 0 && at < bytes)
-        *(uint16_t*)(p + at) = 0;
+__global__ __launch_bounds__(kBlockThreads) void clear_kernel(Clear c) {
+    clear_share(c, blockIdx.x, gridDim.x);
 }
 
 hipError_t launch(const void* fn, uint64_t wgs, uint32_t threads, void** args, hipStream_t st) {
     return hipLaunchKernel(fn, dim3((uint32_t)wgs), dim3(threads), args, 0, st);
 }
 
-hipError_t sort_small(SortArgs& s, uint32_t passes, hipStream_t st) {
-    const void* fn = s.n <= 1024   ? (const void*)&sort_small_kernel<1>
-                     : s.n <= 2048 ? (const void*)&sort_small_kernel<2>
-                     : s.n <= 4096 ? (const void*)&sort_small_kernel<4>
-                                   : (const void*)&sort_small_kernel<8>;
-    void* args[] = {(void*)&s, (void*)&passes};
-    return launch(fn, 1, kSmallThreads, args, st);
+// Share i of `shares` of the table's clearing.
+Clear clear_of(void* grad, uint64_t bytes, uint32_t i, uint32_t shares) {
+    const uint64_t units = bytes / 16, per = (units + shares - 1) / shares;
+    Clear c = {(char*)grad, std::min(units, i * per), std::min(units, (i + 1) * per), 0};
+    if (i + 1 == shares)
+        c.tail = (uint32_t)(bytes % 16);
+    return c;
 }
 
-// Sorts the tokens; *key, *pos get the buffers that hold them in order.
-hipError_t sort(const EmbedGradArgs& a, const Layout& l, bool want_named, const uint32_t** key,
+uint64_t clear_wgs(const Clear& c) {
+    const uint64_t units = kClearBytes / 16, n = (c.hi - c.lo + units - 1) / units;
+    return std::min(kClearWgs, std::max<uint64_t>(n, c.tail ? 1 : 0));
+}
+
+// The range sort that holds n tokens: 1024 K of them.
+const void* sort_range_of(uint32_t n) {
+    static_assert(kRangeTokens == 64 * kRangeThreads, "the largest K");
+    return n <= 1024    ? (const void*)&sort_range_kernel<1>
+           : n <= 2048  ? (const void*)&sort_range_kernel<2>
+           : n <= 4096  ? (const void*)&sort_range_kernel<4>
+           : n <= 8192  ? (const void*)&sort_range_kernel<8>
+           : n <= 16384 ? (const void*)&sort_range_kernel<16>
+           : n <= 32768 ? (const void*)&sort_range_kernel<32>
+                        : (const void*)&sort_range_kernel<64>;
+}
+
+// Sorts the tokens; *key, *pos get the buffers that hold them in order.  The
+// launches also clear clear_bytes of the gradient.
+hipError_t sort(const EmbedGradArgs& a, const Layout& l, uint64_t clear_bytes, const uint32_t** key,
                 const uint32_t** pos, hipStream_t st) {
     char* ws = (char*)a.workspace;
     SortArgs s = {};
@@ -622,36 +772,45 @@ hipError_t sort(const EmbedGradArgs& a, const Layout& l, bool want_named, const 
     s.id64 = a.id64;
     s.n = (uint32_t)a.n_tok;
     s.rows = (uint32_t)a.rows;
-    s.count = (uint32_t*)(ws + l.count);
-    s.named = want_named ? (uint8_t*)(ws + l.named) : nullptr;
     s.runs = (uint32_t*)(ws + l.runs);
-    // Keys run from 0 to rows: as many digits as their bits need, of equal width.
+    s.key_out = (uint32_t*)(ws + l.key[0]);
+    s.pos_out = (uint32_t*)(ws + l.pos[0]);
+    void* args[] = {(void*)&s};
+    if (sorts_by_range(a.n_tok, a.rows)) {
+        // Keys run from 0 to rows.  A workgroup for every 32 tokens, at most
+        // kRangeWgs of them unless that gives one over kRangeBins keys.
+        const uint32_t keys = s.rows + 1;
+        uint32_t wgs = std::max(std::min((s.n + 31) / 32, kRangeWgs),
+                                (keys + kRangeBins - 1) / kRangeBins);
+        s.per_wg = (keys + wgs - 1) / wgs;
+        s.wgs = (keys + s.per_wg - 1) / s.per_wg;
+        s.clear = clear_of(a.grad, clear_bytes, 0, 1);
+        *key = s.key_out;
+        *pos = s.pos_out;
+        return launch(sort_range_of(s.n), s.wgs + clear_wgs(s.clear), kRangeThreads, args, st);
+    }
+    // As many digits as the keys' bits need, of equal width.
     uint32_t bits = 1;
     while ((s.rows >> bits) != 0)
         ++bits;
     const uint32_t passes = (bits + kDigitBits - 1) / kDigitBits;
     s.bits = (bits + passes - 1) / passes;
-    if (a.n_tok <= kSmallTokens) {
-        s.key_out = (uint32_t*)(ws + l.key[0]);
-        s.pos_out = (uint32_t*)(ws + l.pos[0]);
-        *key = s.key_out;
-        *pos = s.pos_out;
-        return sort_small(s, passes, st);
-    }
+    s.count = (uint32_t*)(ws + l.count);
     const uint32_t rounds = (s.n + kSortRound - 1) / kSortRound;
-    s.per_block = (rounds + kSortBlocks - 1) / kSortBlocks * kSortRound;
-    const uint32_t wgs = (s.n + s.per_block - 1) / s.per_block;
-    uint8_t* named = s.named;
+    s.per_wg = (rounds + kSortBlocks - 1) / kSortBlocks * kSortRound;
+    s.wgs = (s.n + s.per_wg - 1) / s.per_wg;
     for (uint32_t p = 0; p < passes; ++p) {
         s.shift = p * s.bits;
         s.key_out = (uint32_t*)(ws + l.key[p & 1]);
         s.pos_out = (uint32_t*)(ws + l.pos[p & 1]);
-        void* args[] = {(void*)&s};
-        hipError_t e = launch((const void*)&sort_count_kernel, wgs, kSortThreads, args, st);
+        s.clear = clear_of(a.grad, clear_bytes, 2 * p, 2 * passes);
+        hipError_t e = launch((const void*)&sort_count_kernel, s.wgs + clear_wgs(s.clear),
+                              kSortThreads, args, st);
         if (e != hipSuccess)
             return e;
-        s.named = p + 1 == passes ? named : nullptr;
-        e = launch((const void*)&sort_scatter_kernel, wgs, kSortThreads, args, st);
+        s.clear = clear_of(a.grad, clear_bytes, 2 * p + 1, 2 * passes);
+        e = launch((const void*)&sort_scatter_kernel, s.wgs + clear_wgs(s.clear), kSortThreads, args,
+                   st);
         if (e != hipSuccess)
             return e;
         s.key_in = s.key_out;
@@ -667,36 +826,29 @@ hipError_t grad_t(const EmbedGradArgs& a, hipStream_t st) {
     const Layout l = layout(a.n_tok, a.rows, a.dim);
     char* ws = (char*)a.workspace;
     SumArgs s = {};
-    hipError_t e = sort(a, l, MODE == kGradWrite, &s.key, &s.pos, st);
+    const uint64_t clear = MODE == kGradWrite ? a.rows * a.dim * (OUT == kF32 ? 4 : 2) : 0;
+    hipError_t e = sort(a, l, clear, &s.key, &s.pos, st);
     if (e != hipSuccess)
         return e;
-    s.named = (const uint8_t*)(ws + l.named);
     s.runs = (uint32_t*)(ws + l.runs);
     s.part = (float*)(ws + l.part);
     s.pitch = l.pitch;
     s.n = (uint32_t)a.n_tok;
+    s.chunk = (uint32_t)l.chunk;
     s.chunks = (uint32_t)l.chunks;
     s.rows = (uint32_t)a.rows;
     s.dim = a.dim;
-    s.col_tiles = (uint32_t)((a.dim + kCols - 1) / kCols);
+    s.col_tiles = (uint32_t)l.col_tiles;
     s.dout = a.dout;
     s.grad = a.grad;
     s.scale = a.scale;
     s.seed = a.seed;
     s.cbase = a.cbase;
-    constexpr uint64_t kMaxWgs = 1 << 20;
-    const uint64_t jobs = (uint64_t)s.chunks * s.col_tiles;
-    s.sum_wgs = (uint32_t)std::min(kMaxWgs, (jobs + 3) / 4);
-    uint64_t clear = 0;
-    if (MODE == kGradWrite) {
-        const uint64_t row_bytes = a.dim * (OUT == kF32 ? 4 : 2);
-        s.clear_rows = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(64, kClearBytes / row_bytes));
-        clear = std::min(kMaxWgs, (a.rows + s.clear_rows - 1) / s.clear_rows);
-    }
+    const uint64_t jobs = l.chunks * l.col_tiles;
     void* args[] = {(void*)&s};
-    e = launch((const void*)&sum_kernel<IN, OUT, MODE, WHOLE>, s.sum_wgs + clear, kBlockThreads, args,
-               st);
-    if (e != hipSuccess || a.n_tok <= 2 * kChunk)
+    e = launch((const void*)&sum_kernel<IN, OUT, MODE, WHOLE>, std::min(kMaxWgs, (jobs + 3) / 4),
+               kBlockThreads, args, st);
+    if (e != hipSuccess || a.n_tok <= 2 * l.chunk)
         return e;  // no run is longer than a chunk and its successor
     return launch((const void*)&join_kernel<OUT, MODE, WHOLE>, std::min<uint64_t>(512, jobs),
                   kJoinThreads, args, st);
@@ -704,7 +856,7 @@ hipError_t grad_t(const EmbedGradArgs& a, hipStream_t st) {
 
 template <int IN, int OUT, int MODE>
 hipError_t grad_m(const EmbedGradArgs& a, hipStream_t st) {
-    return a.dim % 8 == 0 ? grad_t<IN, OUT, MODE, true>(a, st) : grad_t<IN, OUT, MODE, false>(a, st);
+    return a.dim % Cols<OUT>::G == 0 ? grad_t<IN, OUT, MODE, true>(a, st) : grad_t<IN, OUT, MODE, false>(a, st);
 }
 
 template <int IN, int OUT>
@@ -738,11 +890,9 @@ size_t embed_grad_workspace(uint64_t n_tok, uint64_t rows, uint64_t dim) {
 hipError_t launch_embed_grad(const EmbedGradArgs& a, int d_type, int grad_type, int mode,
                              hipStream_t stream) {
     if (a.n_tok == 0) {
-        char* p = (char*)a.grad;
-        uint64_t bytes = a.rows * a.dim * (grad_type == kF32 ? 4 : 2);
-        void* args[] = {(void*)&p, (void*)&bytes};
-        return launch((const void*)&clear_kernel, std::min<uint64_t>(8192, bytes / 4096 + 1),
-                      kBlockThreads, args, stream);
+        Clear c = clear_of(a.grad, a.rows * a.dim * (grad_type == kF32 ? 4 : 2), 0, 1);
+        void* args[] = {(void*)&c};
+        return launch((const void*)&clear_kernel, clear_wgs(c), kBlockThreads, args, stream);
     }
     switch (d_type) {
         case kF32: return grad_in<kF32>(a, grad_type, mode, stream);

@@ -30,20 +30,6 @@ struct NormGeom {
 };
 
 template <int T>
-__device__ __forceinline__ void widen(u4 w, float* x) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (T == kF32) {
-            x[i] = bitsf(v[i]);
-        } else {
-            x[2 * i] = half_lo<T>(v[i]);
-            x[2 * i + 1] = half_hi<T>(v[i]);
-        }
-    }
-}
-
-template <int T>
 __device__ __forceinline__ float load1(const void* p, uint64_t i) {
     if constexpr (T == kF32)
         return ((const float*)p)[i];
@@ -93,16 +79,16 @@ __global__ __launch_bounds__(1024) void sumsq_kernel(NormBatch b, double* out, u
         const void* g = b.g[s];
         const uint64_t n = b.n[s];
         if (base + G::TILE <= n) {
-            u4 w[kNormU];
+            Raw<T, G::VEC> w[kNormU];
 #pragma unroll
             for (int u = 0; u < kNormU; ++u) {
                 const uint64_t i0 = base + (uint64_t)u * G::SUB + (uint64_t)lane * G::VEC;
-                w[u] = ld_stream((const u4*)((const char*)g + i0 * (16 / G::VEC)));
+                w[u] = load_group<T, G::VEC, true, true>(g, i0, G::VEC);
             }
 #pragma unroll
             for (int u = 0; u < kNormU; ++u) {
                 float x[G::VEC];
-                widen<T>(w[u], x);
+                widen<T, G::VEC>(w[u], x);
 #pragma unroll
                 for (int j = 0; j < G::VEC; ++j)
                     acc[j & 3] = __builtin_fma((double)x[j], (double)x[j], acc[j & 3]);
@@ -165,26 +151,21 @@ __global__ __launch_bounds__(kBlockThreads) void clip_kernel(ClipBatch b) {
         if (c == 1.0f && out == g)
             continue;
         if (base + G::TILE <= n) {
-            u4 w[kNormU];
+            Raw<T, G::VEC> w[kNormU];
 #pragma unroll
             for (int u = 0; u < kNormU; ++u) {
                 const uint64_t i0 = base + (uint64_t)u * G::SUB + (uint64_t)lane * G::VEC;
-                w[u] = ld_stream((const u4*)((const char*)g + i0 * (16 / G::VEC)));
+                w[u] = load_group<T, G::VEC, true, true>(g, i0, G::VEC);
             }
 #pragma unroll
             for (int u = 0; u < kNormU; ++u) {
                 const uint64_t i0 = base + (uint64_t)u * G::SUB + (uint64_t)lane * G::VEC;
                 float x[G::VEC];
-                widen<T>(w[u], x);
-                uint32_t o[4];
+                widen<T, G::VEC>(w[u], x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (T == kF32)
-                        o[j] = fbits(c * x[j]);
-                    else
-                        o[j] = pack_products<T>(c * x[2 * j], c * x[2 * j + 1]);
-                }
-                st_stream(u4{o[0], o[1], o[2], o[3]}, (u4*)((char*)out + i0 * (16 / G::VEC)));
+                for (int j = 0; j < G::VEC; ++j)
+                    x[j] = c * x[j];
+                store_group<T, G::VEC, true, true>(narrow<T, G::VEC>(x), out, i0, G::VEC);
             }
         } else {
             for (uint64_t i = base + lane; i < n; i += kWave) {

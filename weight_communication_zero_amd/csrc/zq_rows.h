@@ -1,11 +1,16 @@
-// zq_rows.h -- device access to rows of a [rows, dim] array by groups of eight
-// consecutive elements, shared by the embedding kernels.
+// zq_rows.h -- device access to rows of a [rows, dim] array by groups of G = 4
+// or 8 consecutive elements, shared by the embedding kernels.
 //
-// Where dim is a multiple of 8 every group starts on a 16-byte boundary and is
-// whole (WHOLE).  Otherwise a row may start at any element: a whole group is
-// then read and written through vector types of the element's alignment (the
-// hardware takes unaligned global accesses), and the row's last group, which
-// has fewer elements, one by one.
+// Where dim is a multiple of G every group starts on a boundary of its own size
+// (16 bytes at most) and is whole (WHOLE).  Otherwise a row may start at any
+// element: a whole group is then read and written through vector types of the
+// element's alignment (the hardware takes unaligned global accesses), and the
+// row's last group, which has fewer elements, one by one.
+//
+// NT marks the access nontemporal.  It pays where a wave's instruction covers
+// whole cache lines, and costs where it covers half of each (8 fp32 values a
+// lane take two instructions, each with every other 16 bytes): the line then
+// travels twice.
 #pragma once
 
 #include "zq_device.h"
@@ -13,67 +18,121 @@
 
 namespace zq {
 
-typedef uint32_t u4a2 __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u2a1 __attribute__((ext_vector_type(2), aligned(1)));
-typedef float f4a4 __attribute__((ext_vector_type(4), aligned(4)));
-
-__device__ __forceinline__ uint32_t word(const u4& w, int i) {
-    return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+// Bytes of an element: 4, 2, or 1 for qwZ codes.
+template <int T>
+constexpr int elem_bytes() {
+    return T == kF32 ? 4 : T == kQ8 ? 1 : 2;
 }
 
-// Raw bits of eight elements: 32 bytes for fp32, 16 for the 16-bit types.
-template <int T>
-struct Raw8 {
-    u4 w[T == kF32 ? 2 : 1];
+// The bits of G elements.
+template <int T, int G>
+struct Raw {
+    static constexpr int kWords = G * elem_bytes<T>() / 4;
+    uint32_t w[kWords];
 };
 
-// Elements e .. e + 7 of p, of which the first `left` exist.
-template <int T, bool WHOLE>
-__device__ __forceinline__ Raw8<T> load8(const void* __restrict__ p, uint64_t e, uint32_t left) {
-    Raw8<T> r;
-    if constexpr (WHOLE) {
-        if constexpr (T == kF32) {
-            r.w[0] = ((const u4*)((const float*)p + e))[0];
-            r.w[1] = ((const u4*)((const float*)p + e))[1];
-        } else {
-            r.w[0] = *(const u4*)((const uint16_t*)p + e);
-        }
-    } else if (left >= 8) {
-        if constexpr (T == kF32) {
-            const float* q = (const float*)p + e;
-            r.w[0] = __builtin_bit_cast(u4, (f4)*(const f4a4*)q);
-            r.w[1] = __builtin_bit_cast(u4, (f4)*(const f4a4*)(q + 4));
-        } else {
-            r.w[0] = (u4)*(const u4a2*)((const uint16_t*)p + e);
-        }
-    } else {
-        uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+// N 32-bit words at p, which is aligned to A bytes (NT: to the vector's size).
+template <int N, int A, bool NT>
+__device__ __forceinline__ void load_words(const void* __restrict__ p, uint32_t* w) {
+    constexpr int V = N < 4 ? N : 4;
+    typedef uint32_t vec __attribute__((ext_vector_type(V)));
+    typedef uint32_t vec_a __attribute__((ext_vector_type(V), aligned(A)));
 #pragma unroll
-        for (uint32_t j = 0; j < 7; ++j)
+    for (int i = 0; i < N / V; ++i) {
+        vec v;
+        if constexpr (NT)
+            v = __builtin_nontemporal_load((const vec*)p + i);
+        else
+            v = *((const vec_a*)p + i);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            w[i * V + j] = v[j];
+    }
+}
+
+template <int N, int A, bool NT>
+__device__ __forceinline__ void store_words(const uint32_t* w, void* __restrict__ p) {
+    constexpr int V = N < 4 ? N : 4;
+    typedef uint32_t vec_a __attribute__((ext_vector_type(V), aligned(A)));
+#pragma unroll
+    for (int i = 0; i < N / V; ++i) {
+        if constexpr (NT && V == 4)
+            st_stream(u4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]}, (u4*)p + i);
+        else if constexpr (NT && V == 2)
+            st_stream(u2{w[0], w[1]}, (u2*)p);
+        else if constexpr (NT)
+            st_stream(w[0], (uint32_t*)p);
+        else {
+            vec_a v;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] = w[i * V + j];
+            *((vec_a*)p + i) = v;
+        }
+    }
+}
+
+// Elements e .. e + G - 1 of p, of which the first `left` exist.
+template <int T, int G, bool WHOLE, bool NT>
+__device__ __forceinline__ Raw<T, G> load_group(const void* __restrict__ p, uint64_t e,
+                                                uint32_t left) {
+    constexpr int B = elem_bytes<T>(), N = Raw<T, G>::kWords;
+    const char* q = (const char*)p + e * B;
+    Raw<T, G> r;
+    if constexpr (WHOLE) {
+        load_words<N, (N < 4 ? 4 * N : 16), NT>(q, r.w);
+    } else if (left >= G) {
+        load_words<N, B, false>(q, r.w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            r.w[i] = 0;
+#pragma unroll
+        for (uint32_t j = 0; j < G - 1; ++j)
             if (j < left) {
-                if constexpr (T == kF32)
-                    v[j] = fbits(((const float*)p)[e + j]);
+                if constexpr (B == 4)
+                    r.w[j] = ((const uint32_t*)q)[j];
+                else if constexpr (B == 2)
+                    r.w[j / 2] |= (uint32_t)((const uint16_t*)q)[j] << (16 * (j & 1));
                 else
-                    v[j >> 1] |= (uint32_t)((const uint16_t*)p)[e + j] << (16 * (j & 1));
+                    r.w[j / 4] |= (uint32_t)((const uint8_t*)q)[j] << (8 * (j & 3));
             }
-        r.w[0] = u4{v[0], v[1], v[2], v[3]};
-        if constexpr (T == kF32)
-            r.w[1] = u4{v[4], v[5], v[6], v[7]};
     }
     return r;
 }
 
-template <int T>
-__device__ __forceinline__ void widen8(const Raw8<T>& r, float x[8]) {
+template <int T, int G, bool WHOLE, bool NT>
+__device__ __forceinline__ void store_group(const Raw<T, G>& r, void* __restrict__ p, uint64_t e,
+                                            uint32_t left) {
+    constexpr int B = elem_bytes<T>(), N = Raw<T, G>::kWords;
+    char* q = (char*)p + e * B;
+    if constexpr (WHOLE) {
+        store_words<N, (N < 4 ? 4 * N : 16), NT>(r.w, q);
+    } else if (left >= G) {
+        store_words<N, B, false>(r.w, q);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (T == kF32) {
-            x[i] = bitsf(word(r.w[0], i));
-            x[4 + i] = bitsf(word(r.w[T == kF32 ? 1 : 0], i));
-        } else {
-            x[2 * i] = half_lo<T>(word(r.w[0], i));
-            x[2 * i + 1] = half_hi<T>(word(r.w[0], i));
-        }
+        for (uint32_t j = 0; j < G - 1; ++j)
+            if (j < left) {
+                if constexpr (B == 4)
+                    ((uint32_t*)q)[j] = r.w[j];
+                else
+                    ((uint16_t*)q)[j] = (uint16_t)(r.w[j / 2] >> (16 * (j & 1)));
+            }
+    }
+}
+
+// The elements' values (of codes: the integers).
+template <int T, int G>
+__device__ __forceinline__ void widen(const Raw<T, G>& r, float* x) {
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        if constexpr (T == kF32)
+            x[j] = bitsf(r.w[j]);
+        else if constexpr (T == kQ8)
+            x[j] = (float)((int32_t)(r.w[j / 4] << (24 - 8 * (j & 3))) >> 24);
+        else
+            x[j] = j & 1 ? half_hi<T>(r.w[j / 2]) : half_lo<T>(r.w[j / 2]);
     }
 }
 
@@ -94,48 +153,18 @@ __device__ __forceinline__ uint32_t pack_products(float lo, float hi) {
         return pack_bf16_rne(lo, hi);
 }
 
-// Eight fp32 values in type T's bits, rounded to nearest even.
-template <int T>
-__device__ __forceinline__ Raw8<T> narrow8(const float x[8]) {
-    Raw8<T> r;
-    if constexpr (T == kF32) {
-        r.w[0] = u4{fbits(x[0]), fbits(x[1]), fbits(x[2]), fbits(x[3])};
-        r.w[T == kF32 ? 1 : 0] = u4{fbits(x[4]), fbits(x[5]), fbits(x[6]), fbits(x[7])};
-    } else {
-        r.w[0] = u4{pack_products<T>(x[0], x[1]), pack_products<T>(x[2], x[3]),
-                    pack_products<T>(x[4], x[5]), pack_products<T>(x[6], x[7])};
+// G fp32 values in type T's bits, rounded to nearest even.
+template <int T, int G>
+__device__ __forceinline__ Raw<T, G> narrow(const float* x) {
+    Raw<T, G> r;
+#pragma unroll
+    for (int i = 0; i < Raw<T, G>::kWords; ++i) {
+        if constexpr (T == kF32)
+            r.w[i] = fbits(x[i]);
+        else
+            r.w[i] = pack_products<T>(x[2 * i], x[2 * i + 1]);
     }
     return r;
-}
-
-template <int T, bool WHOLE>
-__device__ __forceinline__ void store8(const Raw8<T>& r, void* __restrict__ p, uint64_t e,
-                                       uint32_t left) {
-    if constexpr (WHOLE) {
-        if constexpr (T == kF32) {
-            st_stream(r.w[0], (u4*)((float*)p + e));
-            st_stream(r.w[T == kF32 ? 1 : 0], (u4*)((float*)p + e + 4));
-        } else {
-            st_stream(r.w[0], (u4*)((uint16_t*)p + e));
-        }
-    } else if (left >= 8) {
-        if constexpr (T == kF32) {
-            float* q = (float*)p + e;
-            *(f4a4*)q = __builtin_bit_cast(f4, r.w[0]);
-            *(f4a4*)(q + 4) = __builtin_bit_cast(f4, r.w[T == kF32 ? 1 : 0]);
-        } else {
-            *(u4a2*)((uint16_t*)p + e) = r.w[0];
-        }
-    } else {
-#pragma unroll
-        for (uint32_t j = 0; j < 7; ++j)
-            if (j < left) {
-                if constexpr (T == kF32)
-                    ((uint32_t*)p)[e + j] = word(r.w[j >> 2], j & 3);
-                else
-                    ((uint16_t*)p)[e + j] = (uint16_t)(word(r.w[0], j >> 1) >> (16 * (j & 1)));
-            }
-    }
 }
 
 // Token id of position t as an unsigned number: negative ids become large, so
