@@ -139,7 +139,7 @@ typedef struct {
  *   workspace  at least zq_grad_sumsq_workspace(n_seg) bytes.
  * Errors: ZQ_ERR_DTYPE; ZQ_ERR_NULL (segs NULL with n_seg > 0, g of a
  * non-empty segment, sumsq, workspace); ZQ_ERR_SIZE (n_seg above 65536,
- * more than 2^41 elements together, a workspace too small); ZQ_ERR_ALIGN;
+ * more than 2^40 elements together, a workspace too small); ZQ_ERR_ALIGN;
  * ZQ_ERR_ALIAS (sumsq or workspace overlapping a tensor or each other;
  * tensors may overlap each other).
  */
@@ -163,7 +163,7 @@ size_t zq_grad_sumsq_workspace(uint32_t n_seg);
  *   max_norm, eps   finite, >= 0 (ZQ_ERR_SIZE otherwise).
  *   norm   one fp32, written with the norm rounded to binary32, or NULL.
  * Errors: ZQ_ERR_DTYPE; ZQ_ERR_NULL (segs, sumsq, g or out of a non-empty
- * segment); ZQ_ERR_SIZE; ZQ_ERR_ALIGN; ZQ_ERR_ALIAS (a written range -- out,
+ * segment); ZQ_ERR_SIZE (also as above); ZQ_ERR_ALIGN; ZQ_ERR_ALIAS (a written range -- out,
  * norm -- overlapping any other range, except out == g of the same segment).
  */
 zq_status zq_grad_clip_batched(const zq_grad_segment *segs, uint32_t n_seg, zq_dtype g_dtype,

@@ -142,8 +142,8 @@ def test_sumsq_refusals():
     ok = seg(G)
     assert call("sumsq", [ok], dt=3) == DTYPE
     assert call("sumsq", [ok], n_seg=65537) == SIZE
-    assert call("sumsq", [seg(G, 2 ** 41 + 1)]) == SIZE
-    assert call("sumsq", [seg(G, 2 ** 40), seg(G, 2 ** 40), seg(G, 1)]) == SIZE
+    assert call("sumsq", [seg(G, 2 ** 40 + 1)]) == SIZE
+    assert call("sumsq", [seg(G, 2 ** 39), seg(G, 2 ** 39), seg(G, 1)]) == SIZE
     assert call("sumsq", [ok], wb=L.zq_grad_sumsq_workspace(1) - 1) == SIZE
     assert call("sumsq", [ok], null=True) == NULL
     assert call("sumsq", [ok], sumsq=None) == NULL and call("sumsq", [ok], ws=None) == NULL
@@ -162,7 +162,7 @@ def test_clip_refusals():
     ok = seg(G)
     assert call("clip", [ok], dt=-2) == DTYPE
     assert call("clip", [ok], n_seg=65537) == SIZE
-    assert call("clip", [seg(G, 2 ** 41 + 1)]) == SIZE
+    assert call("clip", [seg(G, 2 ** 40 + 1)]) == SIZE
     for bad in (-1.0, INF, float("nan")):
         assert call("clip", [ok], max_norm=bad) == SIZE
         assert call("clip", [ok], eps=bad) == SIZE

@@ -16,17 +16,51 @@
 namespace zq {
 namespace {
 
-constexpr int kNormSegs = 128;  // two table entries per lane (SegmentFinder)
+// Segments of a launch: the table travels in the kernel arguments (4 KB).
+constexpr int kSumSegs = 192;
+constexpr int kClipSegs = 144;
+// Vectors of 16 bytes that a lane has in flight.  The clip's waves take one tile
+// each in 1-wave workgroups, XCD by XCD (stream_wave_id), which the dispatcher
+// keeps coming: 0.85 G fp32 elements, norm and clip together, took 1837 us with
+// 2048 looping workgroups, 1640 / 1562 / 1613 us so with 4 / 2 / 1 vectors.
 constexpr int kNormU = 4;
-constexpr uint32_t kNormMaxWgs = 2048;
+constexpr int kClipU = 2;
+constexpr uint32_t kClipMaxWgs = 1u << 24;
+// Workgroups of the sum, each looping over tiles: 0.85 G bf16 elements took
+// 249.4 / 262.5 / 248.9 us with 1024 / 2048 / 4096 of them (6.8 TB/s; a fill
+// writes 6.9), and with plain loads in place of nontemporal ones 274.
+constexpr uint32_t kNormMaxWgs = 4096;
 constexpr uint32_t kNormOneWg = 64;  // most tiles that one workgroup sums by itself
 
-// A tile is 64 lanes x kNormU 16-byte vectors.
-template <int T>
+// A tile is 64 lanes x U 16-byte vectors.
+template <int T, int U>
 struct NormGeom {
     static constexpr int VEC = T == kF32 ? 4 : 8;
     static constexpr int SUB = kWave * VEC;
-    static constexpr int TILE = SUB * kNormU;
+    static constexpr int TILE = SUB * U;
+};
+
+// The segment of a tile, as SegmentFinder gives it, for tables of up to 192
+// segments: lane l holds the cumulative tile counts l, l + 64 and l + 128, and
+// a tile's segment is the number of counts that it has passed.
+template <int N>
+struct TileFinder {
+    static constexpr int E = (N + kWave - 1) / kWave;
+    uint32_t e[E];
+    __device__ __forceinline__ explicit TileFinder(const uint32_t (&ends)[N]) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const uint32_t k = (uint32_t)lane_id() + i * kWave;
+            e[i] = k < N ? ends[k] : UINT32_MAX;
+        }
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t t) const {
+        uint32_t s = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            s += (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(t >= e[i]));
+        return s;
+    }
 };
 
 template <int T>
@@ -38,17 +72,31 @@ __device__ __forceinline__ float load1(const void* p, uint64_t i) {
 }
 
 struct NormBatch {
-    const void* g[kNormSegs];
-    uint64_t n[kNormSegs];
-    uint32_t tile_end[kNormSegs];  // cumulative tiles; unused entries hold UINT32_MAX
+    static constexpr int kSegs = kSumSegs, kU = kNormU;
+    const void* g[kSegs];
+    uint64_t n[kSegs];
+    uint32_t tile_end[kSegs];  // cumulative tiles; unused entries hold UINT32_MAX
     uint32_t total;
 };
 
-// Sum over the wave's lanes, the same tree on every call; lane 0 has it.
+// The value of the lane that a DPP control, or the swap of the two 32-lane
+// halves, pairs with this one.
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xF, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Sum over the wave's lanes, the same tree on every call; every lane has it.
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        v += __shfl_down(v, d);
+    v += dpp<0xB1>(v);   // quad_perm: lane ^ 1
+    v += dpp<0x4E>(v);   // quad_perm: lane ^ 2
+    v += dpp<0x141>(v);  // half mirror: the other quad of eight lanes
+    v += dpp<0x140>(v);  // mirror: the other eight of sixteen
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
     return v;
 }
 
@@ -69,8 +117,8 @@ __device__ __forceinline__ double group_sum(double v) {
 template <int T>
 __global__ __launch_bounds__(1024) void sumsq_kernel(NormBatch b, double* out, uint32_t last,
                                                      uint32_t accumulate) {
-    using G = NormGeom<T>;
-    const SegmentFinder<kNormSegs> find(b.tile_end, (uint32_t)kNormSegs);
+    using G = NormGeom<T, kNormU>;
+    const TileFinder<kSumSegs> find(b.tile_end);
     const int lane = lane_id();
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
     for (size_t ts = wave_id(); ts < b.total; ts += wave_count()) {
@@ -114,6 +162,7 @@ __global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* __restri
                                                           uint64_t n, double* sumsq,
                                                           uint32_t accumulate) {
     double a = 0.0;
+#pragma unroll 4
     for (uint64_t i = threadIdx.x; i < n; i += blockDim.x)
         a += part[i];
     a = group_sum(a);
@@ -122,10 +171,11 @@ __global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* __restri
 }
 
 struct ClipBatch {
-    const void* g[kNormSegs];
-    void* out[kNormSegs];
-    uint64_t n[kNormSegs];
-    uint32_t tile_end[kNormSegs];
+    static constexpr int kSegs = kClipSegs, kU = kClipU;
+    const void* g[kSegs];
+    void* out[kSegs];
+    uint64_t n[kSegs];
+    uint32_t tile_end[kSegs];
     uint32_t total;
     float max_norm, eps;
     const double* sumsq;
@@ -133,16 +183,16 @@ struct ClipBatch {
 };
 
 template <int T>
-__global__ __launch_bounds__(kBlockThreads) void clip_kernel(ClipBatch b) {
-    using G = NormGeom<T>;
+__global__ __launch_bounds__(kWave) void clip_kernel(ClipBatch b) {
+    using G = NormGeom<T, kClipU>;
     const double norm = __builtin_sqrt(*b.sumsq);
     if (b.norm && blockIdx.x == 0 && threadIdx.x == 0)
         *b.norm = (float)norm;
     const double q = (double)b.max_norm / (norm + (double)b.eps);
     const float c = q >= 1.0 ? 1.0f : (float)q;  // a NaN stays one
-    const SegmentFinder<kNormSegs> find(b.tile_end, (uint32_t)kNormSegs);
+    const TileFinder<kClipSegs> find(b.tile_end);
     const int lane = lane_id();
-    for (size_t ts = wave_id(); ts < b.total; ts += wave_count()) {
+    for (size_t ts = stream_wave_id<kWave>(); ts < b.total; ts += wave_count()) {
         const uint32_t t = (uint32_t)ts, s = find(t);
         const uint64_t base = (uint64_t)(t - (s ? b.tile_end[s - 1] : 0u)) * G::TILE;
         const void* g = b.g[s];
@@ -151,14 +201,14 @@ __global__ __launch_bounds__(kBlockThreads) void clip_kernel(ClipBatch b) {
         if (c == 1.0f && out == g)
             continue;
         if (base + G::TILE <= n) {
-            Raw<T, G::VEC> w[kNormU];
+            Raw<T, G::VEC> w[kClipU];
 #pragma unroll
-            for (int u = 0; u < kNormU; ++u) {
+            for (int u = 0; u < kClipU; ++u) {
                 const uint64_t i0 = base + (uint64_t)u * G::SUB + (uint64_t)lane * G::VEC;
                 w[u] = load_group<T, G::VEC, true, true>(g, i0, G::VEC);
             }
 #pragma unroll
-            for (int u = 0; u < kNormU; ++u) {
+            for (int u = 0; u < kClipU; ++u) {
                 const uint64_t i0 = base + (uint64_t)u * G::SUB + (uint64_t)lane * G::VEC;
                 float x[G::VEC];
                 widen<T, G::VEC>(w[u], x);
@@ -179,30 +229,28 @@ __global__ __launch_bounds__(kBlockThreads) void clip_kernel(ClipBatch b) {
     }
 }
 
-template <int T>
-uint64_t tiles_of(uint64_t n) {
-    return (n + NormGeom<T>::TILE - 1) / NormGeom<T>::TILE;
-}
-
 void set_out(NormBatch&, uint32_t, void*) {}
 void set_out(ClipBatch& b, uint32_t k, void* out) { b.out[k] = out; }
 
-// Fills a launch's table from segs[i] on and returns the first segment that
-// the next launch takes.  The ABI layer holds a call to 2^41 elements, so the
-// tiles of a launch (1024 elements at least, one ragged one a segment) stay
-// below 2^32.
+// Fills a launch's table with the non-empty segments from segs[i] on and
+// returns the first segment that the next launch takes.  The ABI layer holds a
+// call to 2^40 elements, so the tiles of a launch (of 512 elements at least,
+// and a ragged one a segment) stay below 2^32.
 template <int T, typename B>
 uint32_t fill(B& b, const GradSegment* segs, uint32_t i, uint32_t n_seg) {
+    constexpr uint64_t kTile = NormGeom<T, B::kU>::TILE;
     uint64_t tiles = 0;
     uint32_t k = 0;
-    for (; i < n_seg && k < (uint32_t)kNormSegs; ++i, ++k) {
+    for (; i < n_seg && k < (uint32_t)B::kSegs; ++i) {
+        if (segs[i].n == 0)
+            continue;
         b.g[k] = segs[i].g;
         b.n[k] = segs[i].n;
         set_out(b, k, segs[i].out);
-        tiles += tiles_of<T>(segs[i].n);
-        b.tile_end[k] = (uint32_t)tiles;
+        tiles += (segs[i].n + kTile - 1) / kTile;
+        b.tile_end[k++] = (uint32_t)tiles;
     }
-    for (; k < (uint32_t)kNormSegs; ++k)
+    for (; k < (uint32_t)B::kSegs; ++k)
         b.tile_end[k] = UINT32_MAX;
     b.total = (uint32_t)tiles;
     return i;
@@ -223,6 +271,8 @@ hipError_t sumsq_t(const GradSegment* segs, uint32_t n_seg, uint32_t accumulate,
         // Few tiles: one workgroup sums them and writes the result, one launch
         // in place of two.
         uint32_t last = first == 0 && i == n_seg && b.total <= kNormOneWg;
+        if (b.total == 0 && !last)
+            continue;
         const uint32_t wgs = last ? 1 : norm_wgs(b.total);
         double* out = last ? sumsq : partials + np;
         void* args[] = {(void*)&b, (void*)&out, (void*)&last, (void*)&accumulate};
@@ -250,8 +300,9 @@ hipError_t clip_t(const GradSegment* segs, uint32_t n_seg, const double* sumsq, 
         i = fill<T>(b, segs, i, n_seg);
         void* args[] = {(void*)&b};
         const hipError_t e =
-            hipLaunchKernel((const void*)&clip_kernel<T>, dim3(std::max(norm_wgs(b.total), 1u)),
-                            dim3(kBlockThreads), args, 0, st);
+            hipLaunchKernel((const void*)&clip_kernel<T>,
+                            dim3(std::min(std::max(b.total, 1u), kClipMaxWgs)), dim3(kWave), args, 0,
+                            st);
         if (e != hipSuccess)
             return e;
     } while (i < n_seg);
@@ -262,7 +313,7 @@ hipError_t clip_t(const GradSegment* segs, uint32_t n_seg, const double* sumsq, 
 
 // One partial for each workgroup of each launch.
 size_t grad_sumsq_workspace(uint32_t n_seg) {
-    const size_t launches = std::max<size_t>(1, (n_seg + (size_t)kNormSegs - 1) / kNormSegs);
+    const size_t launches = std::max<size_t>(1, (n_seg + (size_t)kSumSegs - 1) / kSumSegs);
     return sizeof(double) * kNormMaxWgs * launches;
 }
 

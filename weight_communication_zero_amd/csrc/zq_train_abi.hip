@@ -16,7 +16,7 @@
 namespace {
 
 constexpr uint64_t kMaxElems = (uint64_t)1 << 60;
-constexpr uint64_t kMaxListElems = (uint64_t)1 << 41;  // of a norm or clip call
+constexpr uint64_t kMaxListElems = (uint64_t)1 << 40;  // of a norm or clip call
 constexpr uint64_t kMaxRows = ((uint64_t)1 << 31) - 2;
 constexpr uint64_t kMaxDim = ((uint64_t)1 << 31) - 1;
 constexpr uint64_t kMaxTokens = (uint64_t)1 << 30;
@@ -84,27 +84,93 @@ zq_status lookup(const void* table, int table_type, size_t table_bytes, size_t t
 
 struct Range {
     uintptr_t lo, hi;
-    bool written;
 };
 
-// Whether a written range overlaps any other one (read ranges may overlap).
-bool any_alias(std::vector<Range>& ranges) {
-    std::sort(ranges.begin(), ranges.end(),
-              [](const Range& a, const Range& b) { return a.lo < b.lo; });
-    uintptr_t end_any = 0, end_written = 0;
-    for (const Range& r : ranges) {
-        if (r.lo < (r.written ? end_any : end_written))
+Range range(const void* p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + bytes}; }
+bool meet(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Whether a written range overlaps any other one (read ranges may overlap each
+// other).
+bool alias(std::vector<Range>& read, std::vector<Range>& written) {
+    const auto less = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+    std::sort(read.begin(), read.end(), less);
+    std::sort(written.begin(), written.end(), less);
+    uintptr_t end_read = 0, end_written = 0;
+    size_t r = 0;
+    for (const Range& w : written) {
+        for (; r < read.size() && read[r].lo <= w.lo; ++r) {
+            if (read[r].lo < end_written)
+                return true;
+            end_read = std::max(end_read, read[r].hi);
+        }
+        if (w.lo < end_read || w.lo < end_written)
             return true;
-        end_any = std::max(end_any, r.hi);
-        if (r.written)
-            end_written = std::max(end_written, r.hi);
+        end_written = w.hi;
     }
-    return false;
+    return r < read.size() && read[r].lo < end_written;
 }
 
-void add_range(std::vector<Range>& v, const void* p, size_t bytes, bool written) {
-    if (p && bytes)
-        v.push_back({(uintptr_t)p, (uintptr_t)p + bytes, written});
+// What a norm or clip call's segments read (g, where it is not out) and write
+// (out): the spans they lie in, and whether the written ones come one after
+// the other.  Tensors mostly lie in one buffer in order, and the answer to
+// whether anything overlaps then takes no list and no sorting.
+struct Spans {
+    Range read = {UINTPTR_MAX, 0}, written = {UINTPTR_MAX, 0};
+    bool ordered = true;
+
+    void add_read(const Range& r) { read = {std::min(read.lo, r.lo), std::max(read.hi, r.hi)}; }
+    void add_written(const Range& r) {
+        ordered = ordered && r.lo >= written.hi;
+        written = {std::min(written.lo, r.lo), std::max(written.hi, r.hi)};
+    }
+};
+
+// Checks a list's segments (elements of `esz` bytes; `writes`: out is written).
+zq_status check_list(const zq_grad_segment* segs, uint32_t n_seg, size_t esz, bool writes,
+                     Spans* spans) {
+    uint64_t total = 0;
+    for (uint32_t i = 0; i < n_seg; ++i) {
+        const zq_grad_segment& s = segs[i];
+        if (s.n > kMaxListElems - total)
+            return ZQ_ERR_SIZE;
+        if (s.n == 0)
+            continue;
+        total += s.n;
+        if (!s.g || (writes && !s.out))
+            return ZQ_ERR_NULL;
+        if (!aligned(s.g, 16) || (writes && !aligned(s.out, 16)))
+            return ZQ_ERR_ALIGN;
+        if (!writes || s.out != s.g)
+            spans->add_read(range(s.g, s.n * esz));
+        if (writes)
+            spans->add_written(range(s.out, s.n * esz));
+    }
+    return ZQ_OK;
+}
+
+// Whether a list's written ranges, or one of `more` (of which the first
+// `n_written` are written), overlap another range.
+bool list_alias(const zq_grad_segment* segs, uint32_t n_seg, size_t esz, bool writes,
+                const Spans& spans, const Range* more, uint32_t n_written, uint32_t n_more) {
+    bool apart = spans.ordered && !meet(spans.read, spans.written);
+    for (uint32_t i = 0; apart && i < n_more; ++i) {
+        apart = !meet(more[i], spans.written) && (i >= n_written || !meet(more[i], spans.read));
+        for (uint32_t j = 0; apart && j < std::min(i, n_written); ++j)
+            apart = !meet(more[i], more[j]);
+    }
+    if (apart)
+        return false;
+    std::vector<Range> read(more + n_written, more + n_more), written(more, more + n_written);
+    read.reserve(read.size() + n_seg);
+    written.reserve(written.size() + n_seg);
+    for (uint32_t i = 0; i < n_seg; ++i) {
+        const zq_grad_segment& s = segs[i];
+        if (s.n && (!writes || s.out != s.g))
+            read.push_back(range(s.g, s.n * esz));
+        if (s.n && writes)
+            written.push_back(range(s.out, s.n * esz));
+    }
+    return alias(read, written);
 }
 
 }  // namespace
@@ -213,31 +279,15 @@ zq_status zq_grad_sumsq_batched(const zq_grad_segment* segs, uint32_t n_seg, zq_
         return ZQ_ERR_SIZE;
     if (!aligned(sumsq, 8) || !aligned(workspace, 16))
         return ZQ_ERR_ALIGN;
-    std::vector<Range> ranges;
-    std::vector<zq::GradSegment> dev;
-    ranges.reserve((size_t)n_seg + 2);
-    dev.reserve(n_seg);
-    uint64_t total = 0;
-    add_range(ranges, sumsq, 8, true);
-    add_range(ranges, workspace, need, true);
-    for (uint32_t i = 0; i < n_seg; ++i) {
-        const zq_grad_segment& s = segs[i];
-        if (s.n > kMaxListElems - total)
-            return ZQ_ERR_SIZE;
-        if (s.n == 0)
-            continue;
-        total += s.n;
-        if (!s.g)
-            return ZQ_ERR_NULL;
-        if (!aligned(s.g, 16))
-            return ZQ_ERR_ALIGN;
-        add_range(ranges, s.g, s.n * dtype_bytes(t), false);
-        dev.push_back({s.g, nullptr, s.n});
-    }
-    if (any_alias(ranges))
+    Spans spans;
+    const zq_status st = check_list(segs, n_seg, dtype_bytes(t), false, &spans);
+    if (st != ZQ_OK)
+        return st;
+    const Range more[2] = {range(sumsq, 8), range(workspace, need)};
+    if (list_alias(segs, n_seg, dtype_bytes(t), false, spans, more, 2, 2))
         return ZQ_ERR_ALIAS;
-    return launched(zq::launch_grad_sumsq(dev.data(), (uint32_t)dev.size(), t, accumulate != 0,
-                                          sumsq, (double*)workspace, (hipStream_t)stream));
+    return launched(zq::launch_grad_sumsq(segs, n_seg, t, accumulate != 0, sumsq,
+                                          (double*)workspace, (hipStream_t)stream));
 } catch (const std::bad_alloc&) {
     return ZQ_ERR_LAUNCH;
 }
@@ -255,33 +305,16 @@ zq_status zq_grad_clip_batched(const zq_grad_segment* segs, uint32_t n_seg, zq_d
         return ZQ_ERR_NULL;
     if (!aligned(sumsq, 8) || !aligned(norm, 4))
         return ZQ_ERR_ALIGN;
-    std::vector<Range> ranges;
-    std::vector<zq::GradSegment> dev;
-    ranges.reserve(2 * (size_t)n_seg + 2);
-    dev.reserve(n_seg);
-    uint64_t total = 0;
-    add_range(ranges, sumsq, 8, false);
-    add_range(ranges, norm, 4, true);
-    for (uint32_t i = 0; i < n_seg; ++i) {
-        const zq_grad_segment& s = segs[i];
-        if (s.n > kMaxListElems - total)
-            return ZQ_ERR_SIZE;
-        if (s.n == 0)
-            continue;
-        total += s.n;
-        if (!s.g || !s.out)
-            return ZQ_ERR_NULL;
-        if (!aligned(s.g, 16) || !aligned(s.out, 16))
-            return ZQ_ERR_ALIGN;
-        if (s.out != s.g)
-            add_range(ranges, s.g, s.n * dtype_bytes(t), false);
-        add_range(ranges, s.out, s.n * dtype_bytes(t), true);
-        dev.push_back({s.g, s.out, s.n});
-    }
-    if (any_alias(ranges))
+    Spans spans;
+    const zq_status st = check_list(segs, n_seg, dtype_bytes(t), true, &spans);
+    if (st != ZQ_OK)
+        return st;
+    const Range more[2] = {range(norm, norm ? 4 : 0), range(sumsq, 8)};
+    const uint32_t skip = norm ? 0 : 1;
+    if (list_alias(segs, n_seg, dtype_bytes(t), true, spans, more + skip, 1 - skip, 2 - skip))
         return ZQ_ERR_ALIAS;
-    return launched(zq::launch_grad_clip(dev.data(), (uint32_t)dev.size(), t, sumsq, max_norm, eps,
-                                         norm, (hipStream_t)stream));
+    return launched(zq::launch_grad_clip(segs, n_seg, t, sumsq, max_norm, eps, norm,
+                                         (hipStream_t)stream));
 } catch (const std::bad_alloc&) {
     return ZQ_ERR_LAUNCH;
 }

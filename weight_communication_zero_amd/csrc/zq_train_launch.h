@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/zq_train.h"
 #include "zq_launch.h"
 
 namespace zq {
@@ -46,11 +47,8 @@ size_t embed_grad_workspace(uint64_t n_tok, uint64_t rows, uint64_t dim);
 hipError_t launch_embed_grad(const EmbedGradArgs& a, int d_type, int grad_type, int mode,
                              hipStream_t stream);
 
-struct GradSegment {
-    const void* g;
-    void* out;
-    uint64_t n;
-};
+// One tensor of a norm or clip; n == 0 is skipped.
+using GradSegment = zq_grad_segment;
 
 size_t grad_sumsq_workspace(uint32_t n_seg);
 

@@ -135,8 +135,17 @@ def _p(x) -> int | None:
     return x.data_ptr()
 
 
+# torch's own calls for the current stream's handle and the current device;
+# the public ones build a Stream object (2.7 us a call) and check for
+# initialisation first (0.1 us), which every call here would pay.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -158,6 +167,9 @@ def _need(name: str, t, numel: int, dtypes) -> None:
     contiguous GPU tensor of an accepted dtype holding at least `numel`
     elements, so no kernel can index past a caller's buffer."""
     if t is None or isinstance(t, int):
+        return
+    if (t.is_cuda and t.dtype in dtypes and t.is_contiguous() and t.numel() >= numel
+            and t.get_device() == _device()):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -396,9 +408,10 @@ def _index(t) -> int:
 
 
 def _rows_dim(name: str, t) -> tuple[int, int]:
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions [rows, dim], not {tuple(t.shape)}")
-    return t.shape[0], t.shape[1]
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions [rows, dim], not {tuple(shape)}")
+    return shape
 
 
 def zq_embed_lookup(table, ids, scale: float, out, stream=None) -> None:
@@ -411,8 +424,9 @@ def zq_embed_lookup(table, ids, scale: float, out, stream=None) -> None:
     _need("ids", ids, n, _INDEX)
     _need("out", out, n * dim, _FLOAT)
     _check("zq_embed_lookup",
-           lib.zq_embed_lookup(_p(table), _dtype(table), rows, dim, _p(ids), _index(ids), n, scale,
-                               _p(out), _dtype(out), _stream(stream)))
+           lib.zq_embed_lookup(table.data_ptr(), _dtype(table), rows, dim, ids.data_ptr(),
+                               _index(ids), n, scale, out.data_ptr(), _dtype(out),
+                               _stream(stream)))
 
 
 def zq_embed_lookup_int8(codes, scales, block: int, ids, scale: float, out, stream=None) -> None:
@@ -425,8 +439,9 @@ def zq_embed_lookup_int8(codes, scales, block: int, ids, scale: float, out, stre
     _need("ids", ids, n, _INDEX)
     _need("out", out, n * dim, _FLOAT)
     _check("zq_embed_lookup_int8",
-           lib.zq_embed_lookup_int8(_p(codes), _p(scales), block, rows, dim, _p(ids), _index(ids),
-                                    n, scale, _p(out), _dtype(out), _stream(stream)))
+           lib.zq_embed_lookup_int8(codes.data_ptr(), scales.data_ptr(), block, rows, dim,
+                                    ids.data_ptr(), _index(ids), n, scale, out.data_ptr(),
+                                    _dtype(out), _stream(stream)))
 
 
 def embed_grad_workspace(n_tok: int, rows: int, dim: int) -> int:
@@ -472,6 +487,7 @@ class GradSegmentTable:
             self.dtype = _dtype(g)
             _need("out", out, n, (g.dtype,))
             self.arr[i] = GradSegment(_p(g), _p(out), n)
+        self.workspace = grad_sumsq_workspace(len(self.segments))
         self.ptr = C.cast(self.arr, C.c_void_p)
 
 
@@ -487,12 +503,13 @@ def zq_grad_sumsq_batched(segments, sumsq, workspace, accumulate: bool = False,
     workspace: a uint8 tensor of grad_sumsq_workspace(n_seg) bytes."""
     table = segments if isinstance(segments, GradSegmentTable) else GradSegmentTable(segments)
     _need("sumsq", sumsq, 1, _F64)
-    _need("workspace", workspace, grad_sumsq_workspace(len(table.segments)), _U8)
+    _need("workspace", workspace, table.workspace, _U8)
     _check("zq_grad_sumsq_batched",
            lib.zq_grad_sumsq_batched(table.ptr, len(table.segments),
                                      ZQ_FP32 if table.dtype is None else table.dtype,
                                      1 if accumulate else 0, _p(sumsq), _p(workspace),
-                                     workspace.numel(), _stream(stream)))
+                                     workspace.numel() if workspace is not None else 0,
+                                     _stream(stream)))
 
 
 def zq_grad_clip_batched(segments, sumsq, max_norm: float, eps: float = 1e-6, norm=None,
