@@ -40,11 +40,14 @@ __global__ __launch_bounds__(kBlockThreads) void lookup_kernel(LookupArgs a) {
             tok[u] = t0 + q;
             col[u] = (r - q * per_row) * G;
             in[u] = g0 + (uint64_t)u * kWave + lane < groups;
-            // Loads without branches around them stay in flight together: past
-            // the end the last token is read, and row 0 for an id of no row.
-            const uint64_t id = token_id(a.ids, a.id64, min(tok[u], a.n_tok - 1));
-            there[u] = id < a.rows;
-            row[u] = there[u] ? id : 0;
+        }
+        // Loads without branches around them stay in flight together: past the
+        // end the last token is read, and row 0 for an id of no row.
+        load_ids<kLookU>(a.ids, a.id64, [&](int u) { return min(tok[u], a.n_tok - 1); }, row);
+#pragma unroll
+        for (int u = 0; u < kLookU; ++u) {
+            there[u] = row[u] < a.rows;
+            row[u] = there[u] ? row[u] : 0;
         }
         Raw<IN, G> v[kLookU];
         float s0[kLookU], s1[kLookU];

@@ -11,8 +11,8 @@
 //    to the table.  A longer run leaves fp32 partials: the wave it began in
 //    one, and each later chunk that it reaches one.
 // 3. Join.  The partials of each long run are added in order and written.
-// The write mode clears the whole table in the sort's launches, whose few
-// workgroups leave the memory idle; the sums then overwrite the named rows.
+// In the write mode the sort notes which rows the tokens name, and workgroups of
+// the sum's launch clear the others while the sums wait for their loads.
 // Every row is written by one wave per column group, and the grouping depends
 // on the ids and sizes alone, so equal inputs give equal bits; integer atomics
 // only count.
@@ -26,8 +26,9 @@ namespace {
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr uint32_t kCols = kWave * 8;
 
-// Sort of up to kRangeTokens tokens and kRangeRows rows.
-constexpr uint64_t kRangeTokens = 1 << 16;
+// Sort by ranges: up to kRangeTokens tokens and kRangeRows rows.  At 32768 tokens
+// it takes 15 us, the sort by digits 20 us in four launches.
+constexpr uint64_t kRangeTokens = 1 << 15;
 constexpr uint64_t kRangeRows = 1 << 20;
 constexpr uint32_t kRangeBins = 512;  // most rows a workgroup takes
 constexpr uint32_t kRangeWgs = 64;
@@ -41,9 +42,12 @@ constexpr uint32_t kSortItems = 4;
 constexpr uint32_t kSortRound = kSortThreads * kSortItems;
 constexpr uint32_t kSortBlocks = 256;
 
+
 constexpr uint32_t kJoinThreads = 512;
-constexpr uint64_t kClearBytes = 64 << 10;  // a workgroup clears at a time
-constexpr uint64_t kClearWgs = 256;  // at most, each in a loop
+// A workgroup clears rows of about this size together, with nontemporal stores:
+// 16384 tokens into fp32 [32000, 2048] took 70.2 / 71.7 / 73.1 us with 8 / 16 /
+// 32 KB, and 80.4 with plain stores.
+constexpr uint64_t kClearBytes = 8 << 10;
 constexpr uint64_t kMaxWgs = 1 << 20;
 
 // Tokens of a chunk.  Short chunks give more waves, each with a shorter chain
@@ -64,6 +68,7 @@ bool sorts_by_range(uint64_t n_tok, uint64_t rows) {
 struct Layout {
     uint64_t key[2], pos[2];  // u32 [n_tok] each; the second pair for the sort by digits
     uint64_t count;           // u32 [kSortBlocks][kBins], for the sort by digits
+    uint64_t named;           // one byte per row: some token names it
     uint64_t runs;            // u32 [1 + chunks]: number of long runs, their first chunks
     uint64_t part;            // fp32 [chunks + 1][pitch]: partials of the long runs
     uint64_t pitch, col_tiles, chunk, chunks, bytes;
@@ -87,6 +92,7 @@ Layout layout(uint64_t n_tok, uint64_t rows, uint64_t dim) {
     l.pitch = (dim + 7) / 8 * 8;
     l.key[0] = take(4 * n_tok);
     l.pos[0] = take(4 * n_tok);
+    l.named = take(rows);
     l.runs = take(4 * (2 + n_tok / 8));
     const bool digits = !sorts_by_range(n_tok, rows);
     l.key[1] = digits ? take(4 * n_tok) : 0;
@@ -102,30 +108,10 @@ Layout layout(uint64_t n_tok, uint64_t rows, uint64_t dim) {
     return l;
 }
 
-// A share of the table for a launch to clear: 16-byte units [lo, hi) of p, and
-// the 2-byte units of the table's last, broken one.
-struct Clear {
-    char* p;
-    uint64_t lo, hi;
-    uint32_t tail;  // bytes after unit hi, in the last share
-};
-
-__device__ __forceinline__ void clear_share(const Clear& c, uint32_t wg, uint32_t wgs) {
-    constexpr uint64_t kUnits = kClearBytes / 16;
-    for (uint64_t u = c.lo + wg * kUnits; u < c.hi; u += wgs * kUnits) {
-        const uint64_t end = min(u + kUnits, c.hi);
-        for (uint64_t i = u + threadIdx.x; i < end; i += blockDim.x)
-            st_stream(u4{0, 0, 0, 0}, (u4*)c.p + i);
-    }
-    if (wg == 0 && 2 * threadIdx.x < c.tail)
-        *(uint16_t*)(c.p + c.hi * 16 + 2 * threadIdx.x) = 0;
-}
-
 struct SortArgs {
     const void* ids;
     uint32_t id64;
     uint32_t n, rows;
-    uint32_t wgs;        // workgroups of the sort; later ones clear
     uint32_t per_wg;     // rows (range sort) or tokens (digits: a multiple of kSortRound)
     uint32_t shift, bits;
     const uint32_t* key_in;  // nullptr: the first digit, keys come from ids
@@ -133,15 +119,24 @@ struct SortArgs {
     uint32_t* key_out;
     uint32_t* pos_out;
     uint32_t* count;
+    uint8_t* named;          // nullptr: not wanted
     uint32_t* runs;
-    Clear clear;
 };
 
-__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i) {
-    if (a.key_in)
-        return a.key_in[i];
-    const uint64_t id = token_id(a.ids, a.id64, i);
-    return id < a.rows ? (uint32_t)id : a.rows;
+// Keys of positions at(0) .. at(K - 1): the row, or `rows` for an id of none.
+template <int K, typename F>
+__device__ __forceinline__ void sort_keys(const SortArgs& a, F at, uint32_t* key) {
+    if (a.key_in) {
+#pragma unroll
+        for (int u = 0; u < K; ++u)
+            key[u] = a.key_in[at(u)];
+        return;
+    }
+    uint64_t id[K];
+    load_ids<K>(a.ids, a.id64, at, id);
+#pragma unroll
+    for (int u = 0; u < K; ++u)
+        key[u] = id[u] < a.rows ? (uint32_t)id[u] : a.rows;
 }
 
 // Lanes of the wave, of those in `among`, whose digit equals this lane's.
@@ -212,11 +207,6 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortArgs a) {
     constexpr int B = K < 8 ? K : 8;              // steps between looks at the ring
     constexpr uint32_t kRing = 2 * kWave * B;     // holds 63 + 64 B entries
     static_assert(kRangeBins == kBins, "bins_scan");
-    static_assert(kRangeBins * (uint64_t)K * kWave <= 1ull << 32, "a ring entry's two fields");
-    if (blockIdx.x >= a.wgs) {
-        clear_share(a.clear, blockIdx.x - a.wgs, gridDim.x - a.wgs);
-        return;
-    }
     __shared__ uint32_t cnt[kWaves][kRangeBins];
     __shared__ uint32_t ring_s[kWaves][kRing];
     __shared__ uint32_t tmp[kRangeBins / kWave];
@@ -226,11 +216,15 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortArgs a) {
     const uint32_t v0 = blockIdx.x * a.per_wg;
     const uint32_t bins = min(a.per_wg, a.rows + 1 - v0);
     const uint32_t lo = wave * (K * kWave);
-    uint32_t k[K];  // key - v0: below bins in the range; negative for smaller keys
+    uint32_t k[K];  // key - v0: below bins in the range; larger for smaller keys
+    constexpr int L = K < 16 ? K : 16;  // loads together
 #pragma unroll
-    for (int u = 0; u < K; ++u) {
+    for (int u = 0; u < K; u += L) {
         const uint32_t i = lo + u * kWave + lane;
-        k[u] = i < a.n ? sort_key(a, i) : kNone;
+        sort_keys<L>(a, [&](int j) { return min(i + j * kWave, a.n - 1); }, k + u);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            k[u + j] = i + j * kWave < a.n ? k[u + j] : kNone;
     }
     for (uint32_t i = t; i < kWaves * kRangeBins; i += kRangeThreads)
         (&cnt[0][0])[i] = 0;
@@ -255,6 +249,8 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortArgs a) {
         for (uint32_t w = 0; w < kWaves; ++w)
             sum += cnt[w][t];
     }
+    if (a.named && t < bins && v0 + t < a.rows)
+        a.named[v0 + t] = sum != 0;
     uint32_t at = bins_scan(sum, tmp);
 #pragma unroll
     for (uint32_t w = 0; w < kWaves; ++w)
@@ -309,24 +305,33 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortArgs a) {
 }
 
 // Sort by digits: a stable counting sort, least significant digit first, over
-// at most kSortBlocks workgroups.  Counts one digit of a workgroup's tokens.
+// at most kSortBlocks workgroups.  Counts one digit of a workgroup's tokens; the
+// first digit's launch also clears the row flags, which the last one sets.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
-    if (blockIdx.x >= a.wgs) {
-        clear_share(a.clear, blockIdx.x - a.wgs, gridDim.x - a.wgs);
-        return;
-    }
     __shared__ uint32_t cnt[kBins];
     const uint32_t t = threadIdx.x;
     for (uint32_t i = t; i < kBins; i += kSortThreads)
         cnt[i] = 0;
-    if (!a.key_in && blockIdx.x == 0 && t == 0)
-        a.runs[0] = 0;
+    if (!a.key_in) {
+        if (a.named)
+            for (uint64_t r = (uint64_t)blockIdx.x * kSortThreads + t; r < a.rows;
+                 r += (uint64_t)gridDim.x * kSortThreads)
+                a.named[r] = 0;
+        if (blockIdx.x == 0 && t == 0)
+            a.runs[0] = 0;
+    }
     __syncthreads();
     const uint64_t lo = (uint64_t)blockIdx.x * a.per_wg;
     const uint64_t hi = min(lo + a.per_wg, (uint64_t)a.n);
     const uint32_t mask = (1u << a.bits) - 1;
-    for (uint64_t i = lo + t; i < hi; i += kSortThreads)
-        atomicAdd(&cnt[(sort_key(a, (uint32_t)i) >> a.shift) & mask], 1u);
+    for (uint64_t i = lo + t; i < hi; i += kSortRound) {
+        uint32_t key[kSortItems];
+        sort_keys<kSortItems>(a, [&](int j) { return min(i + j * kSortThreads, hi - 1); }, key);
+#pragma unroll
+        for (uint32_t j = 0; j < kSortItems; ++j)
+            if (i + j * kSortThreads < hi)
+                atomicAdd(&cnt[(key[j] >> a.shift) & mask], 1u);
+    }
     __syncthreads();
     for (uint32_t i = t; i < kBins; i += kSortThreads)
         a.count[blockIdx.x * kBins + i] = cnt[i];
@@ -334,10 +339,6 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
 
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) {
     static_assert(kSortThreads == kBins, "a thread per digit value");
-    if (blockIdx.x >= a.wgs) {
-        clear_share(a.clear, blockIdx.x - a.wgs, gridDim.x - a.wgs);
-        return;
-    }
     constexpr uint32_t kWaves = kSortThreads / kWave;
     __shared__ uint16_t cnt[kWaves][kBins];
     __shared__ uint32_t base[kBins];
@@ -347,7 +348,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) 
     // smaller digits, then those of this digit in earlier workgroups.
     uint32_t total = 0, earlier = 0;
 #pragma unroll 8
-    for (uint32_t b = 0; b < a.wgs; ++b) {
+    for (uint32_t b = 0; b < gridDim.x; ++b) {
         const uint32_t c = a.count[b * kBins + t];
         total += c;
         earlier += b < blockIdx.x ? c : 0;
@@ -361,11 +362,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) 
             (&cnt[0][0])[i] = 0;
         __syncthreads();
         uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems];
+        const uint64_t r0 = r + wave * kWave * kSortItems + lane;
+        sort_keys<kSortItems>(a, [&](int j) { return min(r0 + j * kWave, hi - 1); }, key);
 #pragma unroll
         for (uint32_t i = 0; i < kSortItems; ++i) {
-            const uint64_t at = r + wave * kWave * kSortItems + i * kWave + lane;
-            key[i] = at < hi ? sort_key(a, (uint32_t)at) : kNone;
-            pos[i] = at < hi ? (a.pos_in ? a.pos_in[at] : (uint32_t)at) : 0;
+            const uint64_t at = r0 + i * kWave;
+            key[i] = at < hi ? key[i] : kNone;
+            pos[i] = a.pos_in ? a.pos_in[min(at, hi - 1)] : (uint32_t)at;
         }
 #pragma unroll
         for (uint32_t i = 0; i < kSortItems; ++i) {
@@ -384,13 +387,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) 
         __syncthreads();
 #pragma unroll
         for (uint32_t i = 0; i < kSortItems; ++i) {
-            const uint64_t at = r + wave * kWave * kSortItems + i * kWave + lane;
-            if (at >= hi)
+            if (r0 + i * kWave >= hi)
                 continue;
             const uint32_t d = (key[i] >> a.shift) & mask;
             const uint32_t to = base[d] + cnt[wave][d] + rank[i];
             a.key_out[to] = key[i];
             a.pos_out[to] = pos[i];
+            if (a.named && key[i] < a.rows)
+                a.named[key[i]] = 1;
         }
         __syncthreads();
         base[t] += sum;  // the pads counted in it belong to the last round only
@@ -400,6 +404,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs a) 
 struct SumArgs {
     const uint32_t* key;
     const uint32_t* pos;
+    const uint8_t* named;
     uint32_t* runs;
     float* part;
     uint64_t pitch;
@@ -411,6 +416,8 @@ struct SumArgs {
     void* grad;
     float scale;
     uint64_t seed, cbase;
+    uint32_t sum_wgs;     // the workgroups after these clear rows
+    uint32_t clear_rows;  // rows of such a workgroup, at most 64
 };
 
 // The eight 16-bit random numbers of indices q .. q + 7 (the layout of
@@ -658,10 +665,42 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& a, uint32_t k, uint32_t
         w.sum(p, e, ends | (1ull << (span - 1)), a.part + (uint64_t)(k + 1) * a.pitch, long_end);
 }
 
+// Clears the rows of job j that no token names: a thread per group of G columns,
+// over all the job's rows as one run of groups.
+template <int OUT, bool WHOLE>
+__device__ __forceinline__ void clear_rows(const SumArgs& a, uint32_t j) {
+    constexpr int G = Cols<OUT>::G;
+    const uint32_t r0 = j * a.clear_rows, rows = min(a.clear_rows, a.rows - r0);
+    const uint32_t lane = (uint32_t)lane_id();
+    const uint64_t named = __builtin_amdgcn_ballot_w64(lane < rows && a.named[r0 + lane]);
+    const uint32_t per_row = (uint32_t)((a.dim + G - 1) / G);
+    uint32_t row = threadIdx.x / per_row, group = threadIdx.x % per_row;
+    const uint32_t row_step = kBlockThreads / per_row, group_step = kBlockThreads % per_row;
+    const Raw<OUT, G> zero = {};
+    while (row < rows) {
+        if (!((named >> row) & 1))
+            store_group<OUT, G, WHOLE, true>(zero, a.grad, (uint64_t)(r0 + row) * a.dim + (uint64_t)group * G,
+                                             (uint32_t)a.dim - group * G);
+        row += row_step;
+        group += group_step;
+        if (group >= per_row) {
+            group -= per_row;
+            ++row;
+        }
+    }
+}
+
 template <int IN, int OUT, int MODE, bool WHOLE>
 __global__ __launch_bounds__(kBlockThreads) void sum_kernel(SumArgs a) {
+    if (MODE == kGradWrite && blockIdx.x >= a.sum_wgs) {
+        const uint32_t jobs = (a.rows - 1) / a.clear_rows + 1;
+        for (uint32_t j = blockIdx.x - a.sum_wgs; j < jobs; j += gridDim.x - a.sum_wgs)
+            clear_rows<OUT, WHOLE>(a, j);
+        return;
+    }
     const uint64_t jobs = (uint64_t)a.chunks * a.col_tiles;
-    for (uint64_t j = wave_id(); j < jobs; j += wave_count()) {
+    const uint64_t waves = (uint64_t)a.sum_wgs * (kBlockThreads / kWave);
+    for (uint64_t j = wave_id(); j < jobs; j += waves) {
         const uint32_t k = (uint32_t)(j / a.col_tiles);
         sum_chunk<IN, OUT, MODE, WHOLE>(a, k, (uint32_t)(j - (uint64_t)k * a.col_tiles));
     }
@@ -677,37 +716,54 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(SumArgs a) {
     constexpr int G = Cols<OUT>::G;
     __shared__ float part[kWaves][kCols];
     const uint32_t wave = threadIdx.x / kWave, lane = (uint32_t)lane_id();
+    const uint32_t list = min(blockIdx.x / a.col_tiles, a.chunks - 1);
+    const uint32_t k0 = a.runs[1 + list];  // read beside the number of runs: a guess at most
     const uint64_t jobs = (uint64_t)a.runs[0] * a.col_tiles;
     for (uint64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
-        const uint32_t k = a.runs[1 + j / a.col_tiles];
+        const uint32_t k = j == blockIdx.x ? k0 : a.runs[1 + j / a.col_tiles];
         const uint32_t tile = (uint32_t)(j % a.col_tiles);
-        const uint32_t row = a.key[(k + 2) * a.chunk];
-        // The chunks from k + 2 on that begin with the row: the first one
-        // does, and the keys are sorted, so 64 probes narrow the end down.
-        uint32_t lo = k + 2, hi = a.chunks;  // lo begins with the row; hi does not, or is the end
-        while (hi - lo > 1) {
-            const uint32_t step = (hi - lo + kWave - 1) / kWave;
-            const uint64_t at = (uint64_t)lo + (uint64_t)lane * step;
-            const bool yes = at < hi && a.key[at * a.chunk] == row;
-            const uint32_t c = (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(yes));
-            hi = (uint32_t)min((uint64_t)hi, (uint64_t)lo + (uint64_t)c * step);
-            lo += (c - 1) * step;
+        // The chunks from k + 2 on that begin with the run's row: chunk k + 2 does,
+        // and the keys are sorted, so 64 probes at a time find the end; mostly
+        // within the next 64 chunks.
+        const uint32_t probe = a.key[min(k + 2 + lane, a.chunks - 1) * a.chunk];
+        const uint32_t row = __builtin_amdgcn_readfirstlane(probe);
+        const Cols<OUT> c(tile, (uint32_t)a.dim);
+        RowBits<OUT, OUT> old = {};
+        if constexpr (MODE != kGradWrite)
+            if (wave == 0)
+                old = load_row<OUT, OUT, WHOLE, false>(a.grad, row, a.dim, c);
+        const uint32_t near = (uint32_t)__builtin_popcountll(
+            __builtin_amdgcn_ballot_w64(k + 2 + lane < a.chunks && probe == row));
+        uint32_t hi = k + 2 + near;
+        if (near == kWave) {
+            uint32_t lo = hi - 1;  // begins with the row; hi does not, or is the end
+            hi = a.chunks;
+            while (hi - lo > 1) {
+                const uint32_t step = (hi - lo + kWave - 1) / kWave;
+                const uint64_t at = (uint64_t)lo + (uint64_t)lane * step;
+                const bool yes = at < hi && a.key[at * a.chunk] == row;
+                const uint32_t n = (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(yes));
+                hi = (uint32_t)min((uint64_t)hi, (uint64_t)lo + (uint64_t)n * step);
+                lo += (n - 1) * step;
+            }
         }
         const uint32_t slots = hi - (k + 1);
         const uint32_t s0 = k + 1 + (uint32_t)((uint64_t)slots * wave / kWaves);
         const uint32_t s1 = k + 1 + (uint32_t)((uint64_t)slots * (wave + 1) / kWaves);
-        const Cols<OUT> c(tile, (uint32_t)a.dim);
         float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-        for (uint32_t i = s0; i < s1; ++i) {
-            const float* q = a.part + (uint64_t)i * a.pitch;
+        for (uint32_t i = s0; i < s1; i += 4) {
+            f4 x[4][2];  // four slots in flight; past the end the last one again, not added
 #pragma unroll
-            for (int g = 0; g < 8; g += 4) {
-                const f4 x = *(const f4*)(q + c.col[g / G] + g % G);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[g + e] += x[e];
+            for (uint32_t u = 0; u < 4; ++u) {
+                const float* q = a.part + (uint64_t)min(i + u, s1 - 1) * a.pitch;
+                x[u][0] = *(const f4*)(q + c.col[0]);
+                x[u][1] = *(const f4*)(q + c.col[4 / G] + 4 % G);
             }
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s[e] += i + u < s1 ? x[u][e / 4][e % 4] : 0.0f;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -718,53 +774,40 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(SumArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     s[e] += part[w][e * kWave + lane];
-            RowBits<OUT, OUT> old = {};
-            if constexpr (MODE != kGradWrite)
-                old = load_row<OUT, OUT, WHOLE, false>(a.grad, row, a.dim, c);
             finish<OUT, MODE, WHOLE>(a, s, old, row, c);
         }
         __syncthreads();
     }
 }
 
-// ZQ_GRAD_WRITE without tokens.
-__global__ __launch_bounds__(kBlockThreads) void clear_kernel(Clear c) {
-    clear_share(c, blockIdx.x, gridDim.x);
+// ZQ_GRAD_WRITE without tokens.  One store a thread: 262 MB took 39.7 us so (as
+// long as torch's fill), 45 to 50 us with loops over 16 to 1024 KB a workgroup.
+__global__ __launch_bounds__(kBlockThreads) void clear_kernel(char* p, uint64_t bytes) {
+    const uint64_t units = bytes / 16;
+    for (uint64_t i = (uint64_t)blockIdx.x * kBlockThreads + threadIdx.x; i < units;
+         i += (uint64_t)gridDim.x * kBlockThreads)
+        ((u4*)p)[i] = u4{0, 0, 0, 0};
+    if (blockIdx.x == 0 && 2 * threadIdx.x < bytes % 16)
+        *(uint16_t*)(p + units * 16 + 2 * threadIdx.x) = 0;
 }
 
 hipError_t launch(const void* fn, uint64_t wgs, uint32_t threads, void** args, hipStream_t st) {
     return hipLaunchKernel(fn, dim3((uint32_t)wgs), dim3(threads), args, 0, st);
 }
 
-// Share i of `shares` of the table's clearing.
-Clear clear_of(void* grad, uint64_t bytes, uint32_t i, uint32_t shares) {
-    const uint64_t units = bytes / 16, per = (units + shares - 1) / shares;
-    Clear c = {(char*)grad, std::min(units, i * per), std::min(units, (i + 1) * per), 0};
-    if (i + 1 == shares)
-        c.tail = (uint32_t)(bytes % 16);
-    return c;
-}
-
-uint64_t clear_wgs(const Clear& c) {
-    const uint64_t units = kClearBytes / 16, n = (c.hi - c.lo + units - 1) / units;
-    return std::min(kClearWgs, std::max<uint64_t>(n, c.tail ? 1 : 0));
-}
-
-// The range sort that holds n tokens: 1024 K of them.
+// The range sort that holds n tokens.
 const void* sort_range_of(uint32_t n) {
-    static_assert(kRangeTokens == 64 * kRangeThreads, "the largest K");
+    static_assert(kRangeTokens <= 32 * kRangeThreads, "the largest K");
     return n <= 1024    ? (const void*)&sort_range_kernel<1>
            : n <= 2048  ? (const void*)&sort_range_kernel<2>
            : n <= 4096  ? (const void*)&sort_range_kernel<4>
            : n <= 8192  ? (const void*)&sort_range_kernel<8>
            : n <= 16384 ? (const void*)&sort_range_kernel<16>
-           : n <= 32768 ? (const void*)&sort_range_kernel<32>
-                        : (const void*)&sort_range_kernel<64>;
+                        : (const void*)&sort_range_kernel<32>;
 }
 
-// Sorts the tokens; *key, *pos get the buffers that hold them in order.  The
-// launches also clear clear_bytes of the gradient.
-hipError_t sort(const EmbedGradArgs& a, const Layout& l, uint64_t clear_bytes, const uint32_t** key,
+// Sorts the tokens; *key, *pos get the buffers that hold them in order.
+hipError_t sort(const EmbedGradArgs& a, const Layout& l, bool want_named, const uint32_t** key,
                 const uint32_t** pos, hipStream_t st) {
     char* ws = (char*)a.workspace;
     SortArgs s = {};
@@ -772,6 +815,7 @@ hipError_t sort(const EmbedGradArgs& a, const Layout& l, uint64_t clear_bytes, c
     s.id64 = a.id64;
     s.n = (uint32_t)a.n_tok;
     s.rows = (uint32_t)a.rows;
+    s.named = want_named ? (uint8_t*)(ws + l.named) : nullptr;
     s.runs = (uint32_t*)(ws + l.runs);
     s.key_out = (uint32_t*)(ws + l.key[0]);
     s.pos_out = (uint32_t*)(ws + l.pos[0]);
@@ -780,14 +824,12 @@ hipError_t sort(const EmbedGradArgs& a, const Layout& l, uint64_t clear_bytes, c
         // Keys run from 0 to rows.  A workgroup for every 32 tokens, at most
         // kRangeWgs of them unless that gives one over kRangeBins keys.
         const uint32_t keys = s.rows + 1;
-        uint32_t wgs = std::max(std::min((s.n + 31) / 32, kRangeWgs),
-                                (keys + kRangeBins - 1) / kRangeBins);
-        s.per_wg = (keys + wgs - 1) / wgs;
-        s.wgs = (keys + s.per_wg - 1) / s.per_wg;
-        s.clear = clear_of(a.grad, clear_bytes, 0, 1);
+        const uint32_t want = std::max(std::min((s.n + 31) / 32, kRangeWgs),
+                                       (keys + kRangeBins - 1) / kRangeBins);
+        s.per_wg = (keys + want - 1) / want;
         *key = s.key_out;
         *pos = s.pos_out;
-        return launch(sort_range_of(s.n), s.wgs + clear_wgs(s.clear), kRangeThreads, args, st);
+        return launch(sort_range_of(s.n), (keys + s.per_wg - 1) / s.per_wg, kRangeThreads, args, st);
     }
     // As many digits as the keys' bits need, of equal width.
     uint32_t bits = 1;
@@ -798,19 +840,17 @@ hipError_t sort(const EmbedGradArgs& a, const Layout& l, uint64_t clear_bytes, c
     s.count = (uint32_t*)(ws + l.count);
     const uint32_t rounds = (s.n + kSortRound - 1) / kSortRound;
     s.per_wg = (rounds + kSortBlocks - 1) / kSortBlocks * kSortRound;
-    s.wgs = (s.n + s.per_wg - 1) / s.per_wg;
+    const uint32_t wgs = (s.n + s.per_wg - 1) / s.per_wg;
+    uint8_t* named = s.named;
     for (uint32_t p = 0; p < passes; ++p) {
         s.shift = p * s.bits;
         s.key_out = (uint32_t*)(ws + l.key[p & 1]);
         s.pos_out = (uint32_t*)(ws + l.pos[p & 1]);
-        s.clear = clear_of(a.grad, clear_bytes, 2 * p, 2 * passes);
-        hipError_t e = launch((const void*)&sort_count_kernel, s.wgs + clear_wgs(s.clear),
-                              kSortThreads, args, st);
+        hipError_t e = launch((const void*)&sort_count_kernel, wgs, kSortThreads, args, st);
         if (e != hipSuccess)
             return e;
-        s.clear = clear_of(a.grad, clear_bytes, 2 * p + 1, 2 * passes);
-        e = launch((const void*)&sort_scatter_kernel, s.wgs + clear_wgs(s.clear), kSortThreads, args,
-                   st);
+        s.named = p + 1 == passes ? named : nullptr;
+        e = launch((const void*)&sort_scatter_kernel, wgs, kSortThreads, args, st);
         if (e != hipSuccess)
             return e;
         s.key_in = s.key_out;
@@ -826,10 +866,10 @@ hipError_t grad_t(const EmbedGradArgs& a, hipStream_t st) {
     const Layout l = layout(a.n_tok, a.rows, a.dim);
     char* ws = (char*)a.workspace;
     SumArgs s = {};
-    const uint64_t clear = MODE == kGradWrite ? a.rows * a.dim * (OUT == kF32 ? 4 : 2) : 0;
-    hipError_t e = sort(a, l, clear, &s.key, &s.pos, st);
+    hipError_t e = sort(a, l, MODE == kGradWrite, &s.key, &s.pos, st);
     if (e != hipSuccess)
         return e;
+    s.named = (const uint8_t*)(ws + l.named);
     s.runs = (uint32_t*)(ws + l.runs);
     s.part = (float*)(ws + l.part);
     s.pitch = l.pitch;
@@ -845,9 +885,15 @@ hipError_t grad_t(const EmbedGradArgs& a, hipStream_t st) {
     s.seed = a.seed;
     s.cbase = a.cbase;
     const uint64_t jobs = l.chunks * l.col_tiles;
+    s.sum_wgs = (uint32_t)std::min(kMaxWgs, (jobs + 3) / 4);
+    uint64_t wgs = s.sum_wgs;
+    if (MODE == kGradWrite) {
+        const uint64_t row_bytes = a.dim * (OUT == kF32 ? 4 : 2);
+        s.clear_rows = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(kWave, kClearBytes / row_bytes));
+        wgs += std::min(kMaxWgs, (a.rows - 1) / s.clear_rows + 1);
+    }
     void* args[] = {(void*)&s};
-    e = launch((const void*)&sum_kernel<IN, OUT, MODE, WHOLE>, std::min(kMaxWgs, (jobs + 3) / 4),
-               kBlockThreads, args, st);
+    e = launch((const void*)&sum_kernel<IN, OUT, MODE, WHOLE>, wgs, kBlockThreads, args, st);
     if (e != hipSuccess || a.n_tok <= 2 * l.chunk)
         return e;  // no run is longer than a chunk and its successor
     return launch((const void*)&join_kernel<OUT, MODE, WHOLE>, std::min<uint64_t>(512, jobs),
@@ -890,9 +936,11 @@ size_t embed_grad_workspace(uint64_t n_tok, uint64_t rows, uint64_t dim) {
 hipError_t launch_embed_grad(const EmbedGradArgs& a, int d_type, int grad_type, int mode,
                              hipStream_t stream) {
     if (a.n_tok == 0) {
-        Clear c = clear_of(a.grad, a.rows * a.dim * (grad_type == kF32 ? 4 : 2), 0, 1);
-        void* args[] = {(void*)&c};
-        return launch((const void*)&clear_kernel, clear_wgs(c), kBlockThreads, args, stream);
+        char* p = (char*)a.grad;
+        uint64_t bytes = a.rows * a.dim * (grad_type == kF32 ? 4 : 2);
+        void* args[] = {(void*)&p, (void*)&bytes};
+        return launch((const void*)&clear_kernel, std::min(kMaxWgs, bytes / 4096 + 1), kBlockThreads,
+                      args, stream);
     }
     switch (d_type) {
         case kF32: return grad_in<kF32>(a, grad_type, mode, stream);

@@ -162,9 +162,15 @@ __global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* __restri
                                                           uint64_t n, double* sumsq,
                                                           uint32_t accumulate) {
     double a = 0.0;
-#pragma unroll 4
-    for (uint64_t i = threadIdx.x; i < n; i += blockDim.x)
-        a += part[i];
+    for (uint64_t i = threadIdx.x; i < n; i += 4 * blockDim.x) {
+        double v[4];  // four in flight; past the end the last one again, not added
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u)
+            v[u] = part[min(i + u * blockDim.x, n - 1)];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u)
+            a += i + u * blockDim.x < n ? v[u] : 0.0;
+    }
     a = group_sum(a);
     if (threadIdx.x == 0)
         *sumsq = accumulate ? *sumsq + a : a;

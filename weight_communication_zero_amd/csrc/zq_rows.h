@@ -167,11 +167,25 @@ __device__ __forceinline__ Raw<T, G> narrow(const float* x) {
     return r;
 }
 
-// Token id of position t as an unsigned number: negative ids become large, so
-// one comparison with the number of rows tells whether it names a row.
-__device__ __forceinline__ uint64_t token_id(const void* __restrict__ ids, uint32_t id64,
-                                             uint64_t t) {
-    return id64 ? ((const uint64_t*)ids)[t] : (uint64_t)(int64_t)((const int32_t*)ids)[t];
+// Token ids of positions at(0) .. at(K - 1) as unsigned numbers: negative ids
+// become large, so one comparison with the number of rows tells whether an id
+// names a row.  The loads stand together behind the one branch on the type.
+template <int K, typename F>
+__device__ __forceinline__ void load_ids(const void* __restrict__ ids, uint32_t id64, F at,
+                                         uint64_t* id) {
+    if (id64) {
+#pragma unroll
+        for (int u = 0; u < K; ++u)
+            id[u] = ((const uint64_t*)ids)[at(u)];
+    } else {
+        int32_t v[K];
+#pragma unroll
+        for (int u = 0; u < K; ++u)
+            v[u] = ((const int32_t*)ids)[at(u)];
+#pragma unroll
+        for (int u = 0; u < K; ++u)
+            id[u] = (uint64_t)(int64_t)v[u];
+    }
 }
 
 }  // namespace zq
