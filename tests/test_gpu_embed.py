@@ -185,7 +185,8 @@ def test_grad(mode, gt, dt, n, rows, dim, kind):
 
 
 @pytest.mark.parametrize("n", [2, 31, 32, 33, 63, 64, 65, 95, 96, 97, 128, 129, 160, 1000, 2048, 2049, 4096, 4097,
-                               8192, 8193, 16384, 20000])
+                               8192, 8193, 16384, 20000,
+                               32768, 32769, 70000])
 @pytest.mark.parametrize("kind", ["one", "zipf", "mixed", "runs"])
 def test_grad_run_lengths(n, kind):
     """Runs that end at, before and after every chunk border, both sorts, and
@@ -212,7 +213,7 @@ def test_grad_run_lengths(n, kind):
 @pytest.mark.parametrize("rows", [1, 2, 255, 511, 512, 513, 50257, 262143, 262144, 300001, 2 ** 27 + 5])
 @pytest.mark.parametrize("n", [300, 9000])
 def test_grad_vocabularies(rows, n):
-    """One to four digits of the sort, both sorts; the largest and smallest row
+    """Ranges of one row to 512 rows, one to four digits, both sorts; the largest and smallest row
     are named, and positions of equal ids keep their order (a sum of values that
     cancel only in that order)."""
     dim = 2
@@ -234,6 +235,9 @@ def test_grad_vocabularies(rows, n):
     keep = torch.ones(rows, dtype=torch.bool, device="cuda")
     keep[named.cuda()] = False
     assert bool((grad[keep] == 5.0).all())
+    written = torch.full((rows, dim), math.nan, device="cuda")
+    zq.zq_embed_grad(dout.cuda(), ids.cuda(), 1.0, written, zq.ZQ_GRAD_WRITE, ws)
+    assert torch.equal(written, exp - 5.0)
     assert torch.equal(grad, exp)
 
 

@@ -152,14 +152,14 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+_DTYPES = {torch.float32: ZQ_FP32, torch.bfloat16: ZQ_BF16, torch.float16: ZQ_FP16}
+
+
 def _dtype(t) -> int:
-    if t.dtype == torch.float32:
-        return ZQ_FP32
-    if t.dtype == torch.bfloat16:
-        return ZQ_BF16
-    if t.dtype == torch.float16:
-        return ZQ_FP16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return d
 
 
 def _need(name: str, t, numel: int, dtypes) -> None:
