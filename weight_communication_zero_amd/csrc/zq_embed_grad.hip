@@ -16,6 +16,12 @@
 // Every row is written by one wave per column group, and the grouping depends
 // on the ids and sizes alone, so equal inputs give equal bits; integer atomics
 // only count.
+//
+// Bound by memory where there is much of it: 32768 bf16 tokens x 4096 added into
+// fp32 move 557 MB in the sum's 119 us (4.7 TB/s, a copy's rate); counters show no
+// byte twice but the partials'.  Around it the sort takes 15 us and the join 8;
+// with 8192 tokens x 768 the three launches take 6 + 11 + 5 us, each little more
+// than its start and one chain of dependent reads.
 #include <algorithm>
 
 #include "zq_rows.h"
@@ -50,9 +56,21 @@ constexpr uint32_t kJoinThreads = 512;
 constexpr uint64_t kClearBytes = 8 << 10;
 constexpr uint64_t kMaxWgs = 1 << 20;
 
-// Tokens of a chunk.  Short chunks give more waves, each with a shorter chain
-// of loads and stores; long ones leave fewer partials of long runs.
-constexpr uint64_t kWantWaves = 8192;
+// Threads of a sum workgroup, whose waves work apart.  Adding, 128 beat 256 by up
+// to 1.5 % and 512 by 3 to 6 %; writing, where most workgroups clear rows, 256
+// beat 64 / 128 / 512 by 5 / 3 / 5 %.
+template <int MODE>
+constexpr uint32_t sum_threads() {
+    return MODE == kGradWrite ? 256 : 128;
+}
+
+// Tokens of a chunk: 32, or as many less (16, 8) as it takes for kWantWaves waves.
+// Short chunks give more waves, each with a shorter chain of loads and stores;
+// long ones leave fewer partials of long runs.  With 4096 / 8192 / 16384 waves
+// wanted, 16384 tokens written into fp32 [32000, 2048] took 67.5 / 70.4 / 70.4
+// us, 32768 added into [32000, 4096] 144.4 / 144.4 / 148.8, 200000 added into
+// [32000, 1024] 176 / 176 / 196.
+constexpr uint64_t kWantWaves = 4096;
 uint32_t chunk_tokens(uint64_t n_tok, uint64_t col_tiles) {
     for (uint32_t c = 32; c > 8; c /= 2)
         if ((n_tok + c - 1) / c * col_tiles >= kWantWaves)
@@ -670,12 +688,13 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& a, uint32_t k, uint32_t
 template <int OUT, bool WHOLE>
 __device__ __forceinline__ void clear_rows(const SumArgs& a, uint32_t j) {
     constexpr int G = Cols<OUT>::G;
+    constexpr uint32_t kThreads = sum_threads<kGradWrite>();
     const uint32_t r0 = j * a.clear_rows, rows = min(a.clear_rows, a.rows - r0);
     const uint32_t lane = (uint32_t)lane_id();
     const uint64_t named = __builtin_amdgcn_ballot_w64(lane < rows && a.named[r0 + lane]);
     const uint32_t per_row = (uint32_t)((a.dim + G - 1) / G);
     uint32_t row = threadIdx.x / per_row, group = threadIdx.x % per_row;
-    const uint32_t row_step = kBlockThreads / per_row, group_step = kBlockThreads % per_row;
+    const uint32_t row_step = kThreads / per_row, group_step = kThreads % per_row;
     const Raw<OUT, G> zero = {};
     while (row < rows) {
         if (!((named >> row) & 1))
@@ -691,7 +710,7 @@ __device__ __forceinline__ void clear_rows(const SumArgs& a, uint32_t j) {
 }
 
 template <int IN, int OUT, int MODE, bool WHOLE>
-__global__ __launch_bounds__(kBlockThreads) void sum_kernel(SumArgs a) {
+__global__ __launch_bounds__(sum_threads<MODE>()) void sum_kernel(SumArgs a) {
     if (MODE == kGradWrite && blockIdx.x >= a.sum_wgs) {
         const uint32_t jobs = (a.rows - 1) / a.clear_rows + 1;
         for (uint32_t j = blockIdx.x - a.sum_wgs; j < jobs; j += gridDim.x - a.sum_wgs)
@@ -699,7 +718,7 @@ __global__ __launch_bounds__(kBlockThreads) void sum_kernel(SumArgs a) {
         return;
     }
     const uint64_t jobs = (uint64_t)a.chunks * a.col_tiles;
-    const uint64_t waves = (uint64_t)a.sum_wgs * (kBlockThreads / kWave);
+    const uint64_t waves = (uint64_t)a.sum_wgs * (sum_threads<MODE>() / kWave);
     for (uint64_t j = wave_id(); j < jobs; j += waves) {
         const uint32_t k = (uint32_t)(j / a.col_tiles);
         sum_chunk<IN, OUT, MODE, WHOLE>(a, k, (uint32_t)(j - (uint64_t)k * a.col_tiles));
@@ -885,7 +904,8 @@ hipError_t grad_t(const EmbedGradArgs& a, hipStream_t st) {
     s.seed = a.seed;
     s.cbase = a.cbase;
     const uint64_t jobs = l.chunks * l.col_tiles;
-    s.sum_wgs = (uint32_t)std::min(kMaxWgs, (jobs + 3) / 4);
+    constexpr uint32_t kThreads = sum_threads<MODE>(), kWaves = kThreads / kWave;
+    s.sum_wgs = (uint32_t)std::min(kMaxWgs, (jobs + kWaves - 1) / kWaves);
     uint64_t wgs = s.sum_wgs;
     if (MODE == kGradWrite) {
         const uint64_t row_bytes = a.dim * (OUT == kF32 ? 4 : 2);
@@ -893,7 +913,7 @@ hipError_t grad_t(const EmbedGradArgs& a, hipStream_t st) {
         wgs += std::min(kMaxWgs, (a.rows - 1) / s.clear_rows + 1);
     }
     void* args[] = {(void*)&s};
-    e = launch((const void*)&sum_kernel<IN, OUT, MODE, WHOLE>, wgs, kBlockThreads, args, st);
+    e = launch((const void*)&sum_kernel<IN, OUT, MODE, WHOLE>, wgs, kThreads, args, st);
     if (e != hipSuccess || a.n_tok <= 2 * l.chunk)
         return e;  // no run is longer than a chunk and its successor
     return launch((const void*)&join_kernel<OUT, MODE, WHOLE>, std::min<uint64_t>(512, jobs),

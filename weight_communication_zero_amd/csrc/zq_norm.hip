@@ -7,8 +7,12 @@
 // exact there and cannot overflow, and the order of the additions (tiles dealt
 // round robin to a fixed number of waves, a tree in the wave and the
 // workgroup, the workgroups' partials in a fixed order) depends on the
-// segments' sizes alone, so equal inputs give equal bits.  The sum reads
-// 4 / 2 B/elem, the clip reads and writes them.  No atomics.
+// segments' sizes alone, so equal inputs give equal bits.  No atomics.
+//
+// Both are bound by memory.  The sum reads 4 / 2 B/elem: 0.85 G elements in 492 us
+// (fp32) or 246 (bf16), 6.9 TB/s.  The clip reads and writes them: 1071 us in
+// fp32, 6.4 TB/s.  Small lists are bound by the launches: 29 MB of fp16 in 111
+// tensors take 8 + 2.5 us (sum and join) and 13 us (clip).
 #include <algorithm>
 
 #include "zq_rows.h"
