@@ -210,7 +210,8 @@ def test_grad_run_lengths(n, kind):
     assert torch.equal(got.cpu(), exp)
 
 
-@pytest.mark.parametrize("rows", [1, 2, 255, 511, 512, 513, 50257, 262143, 262144, 300001, 2 ** 27 + 5])
+@pytest.mark.parametrize("rows", [1, 2, 255, 511, 512, 513, 50257, 262143, 262144, 300001, 500003, 2 ** 20,
+                                  2 ** 27 + 5])
 @pytest.mark.parametrize("n", [300, 9000])
 def test_grad_vocabularies(rows, n):
     """Ranges of one row to 512 rows, one to four digits, both sorts; the largest and smallest row

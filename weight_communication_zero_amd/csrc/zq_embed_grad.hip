@@ -32,10 +32,14 @@ namespace {
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr uint32_t kCols = kWave * 8;
 
-// Sort by ranges: up to kRangeTokens tokens and kRangeRows rows.  At 32768 tokens
-// it takes 15 us, the sort by digits 20 us in four launches.
+// Sort by ranges: its workgroups, one for every kRangeBins rows at least, each
+// read all the tokens.  A whole gradient call (16 columns) took, by ranges / by
+// digits: 32768 tokens 31.8 / 37.7 us with 2^17 rows, 40.9 / 37.7 with 2^18; 8192
+// tokens 29.1 / 36.9 with 2^19, 45.4 / 37.4 with 2^20; 2048 tokens 25.0 / 31.2
+// with 2^20; and 65536 tokens into [32000, 1024] 87.5 / 79.0.
 constexpr uint64_t kRangeTokens = 1 << 15;
 constexpr uint64_t kRangeRows = 1 << 20;
+constexpr uint64_t kRangeWork = 1ull << 32;  // tokens times rows
 constexpr uint32_t kRangeBins = 512;  // most rows a workgroup takes
 constexpr uint32_t kRangeWgs = 64;
 constexpr uint32_t kRangeThreads = 1024;
@@ -79,7 +83,7 @@ uint32_t chunk_tokens(uint64_t n_tok, uint64_t col_tiles) {
 }
 
 bool sorts_by_range(uint64_t n_tok, uint64_t rows) {
-    return n_tok <= kRangeTokens && rows <= kRangeRows;
+    return n_tok <= kRangeTokens && rows <= kRangeRows && n_tok * rows <= kRangeWork;
 }
 
 // How the caller's workspace is laid out; every part on a 256-byte boundary.
