@@ -16,6 +16,9 @@
  *            (per-tensor vector_add on the reduced shard, then zeroing) and of
  *            llmc/cuda_utils.cuh (vector_add with stochastic rounding).
  *
+ * zq_train.h continues this ABI (same library, same conventions) with the two
+ * ends of the step: embedding lookup and gradient, gradient norm and clipping.
+ *
  * Conventions shared by every compute entry point
  *   - Buffers are DEVICE pointers on the current HIP device unless stated.
  *     The caller allocates and frees everything; libzq never allocates,

@@ -127,14 +127,17 @@ def test_lookup_many_tokens():
 
 
 def check_grad(dout, ids, scale, old, got, mode, gt):
-    """`got` against the sums in 64 bits (the bound in this file's header)."""
+    """`got` against the sums in 64 bits (the bound in this file's header), on
+    the device that dout is on."""
     rows, dim = old.shape
-    dout, ids, got = dout.cpu().double(), ids.cpu().long().reshape(-1), got.cpu()
+    dev = dout.device
+    dout, ids, got, old = dout.double(), ids.to(dev).long().reshape(-1), got.to(dev), old.to(dev)
     there = (ids >= 0) & (ids < rows)
-    s = torch.zeros(rows, dim, dtype=torch.float64).index_add_(0, ids[there], dout[there])
-    a = torch.zeros(rows, dim, dtype=torch.float64).index_add_(0, ids[there], dout[there].abs())
+    zero = torch.zeros(rows, dim, dtype=torch.float64, device=dev)
+    s = zero.index_add(0, ids[there], dout[there])
+    a = zero.index_add(0, ids[there], dout[there].abs())
     count = torch.bincount(ids[there], minlength=rows).double()[:, None]
-    base = torch.zeros(rows, dim, dtype=torch.float64) if mode == zq.ZQ_GRAD_WRITE else old.cpu().double()
+    base = zero if mode == zq.ZQ_GRAD_WRITE else old.double()
     scale = float(np.float32(scale))
     exact = base + scale * s
     bound = (count + 3) * 2.0 ** -24 * (abs(scale) * a + base.abs()) + TINY[gt]
@@ -148,7 +151,7 @@ def check_grad(dout, ids, scale, old, got, mode, gt):
     assert bad.numel() == 0, (bad[0].tolist(), got[tuple(bad[0])].item(), exact[tuple(bad[0])].item(),
                               bound[tuple(bad[0])].item(), len(bad))
     untouched = count[:, 0] == 0
-    exp = torch.zeros(rows, dim, dtype=T[gt]) if mode == zq.ZQ_GRAD_WRITE else old.cpu()
+    exp = torch.zeros_like(old) if mode == zq.ZQ_GRAD_WRITE else old
     assert same(got[untouched], exp[untouched])
 
 
@@ -184,9 +187,43 @@ def test_grad(mode, gt, dt, n, rows, dim, kind):
     check_grad(dout, ids, 0.7, old, got, MODE[mode], gt)
 
 
+@pytest.mark.parametrize("mode,gt", [("write", "fp32"), ("write", "fp16"), ("add", "fp32"), ("add", "bf16"),
+                                     ("add_sr", "bf16")])
+@pytest.mark.parametrize("n,rows,dim", [(9000, 3000, 1544), (24000, 3000, 1545), (24000, 700, 2048),
+                                        (40000, 3000, 1544), (36000, 40, 1001)])
+def test_grad_of_many_tokens(mode, gt, n, rows, dim):
+    """Chunks of 8, 16 and 32 tokens, several column groups, long and short runs."""
+    g = torch.Generator(device="cuda").manual_seed(n + dim)
+    dout = torch.randn(n, dim, generator=g, device="cuda").bfloat16()
+    old = torch.randn(rows, dim, generator=g, device="cuda").to(T[gt])
+    ids = make_ids(n, rows, torch.int64, n)
+    got = run_grad(dout, ids, 0.3, old, MODE[mode], seed=n, base=dim)
+    check_grad(dout, ids, 0.3, old, got, MODE[mode], gt)
+
+
+SWEEP = np.random.default_rng(2024)
+
+
+def draw():
+    n = int(2 ** SWEEP.uniform(0, 14))
+    return (n, int(2 ** SWEEP.uniform(0, 12)), int(2 ** SWEEP.uniform(0, 11 if n < 3000 else 8)),
+            ["fp32", "bf16", "fp16"][SWEEP.integers(3)], *MODES[SWEEP.integers(len(MODES))],
+            ["one", "zipf", "mixed", "none"][SWEEP.choice(4, p=[0.1, 0.4, 0.45, 0.05])], int(SWEEP.integers(1 << 40)))
+
+
+@pytest.mark.parametrize("n,rows,dim,dt,mode,gt,kind,seed", [draw() for _ in range(96)])
+def test_grad_random_sweep(n, rows, dim, dt, mode, gt, kind, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dout = torch.randn(n, dim, generator=g, device="cuda").to(T[dt])
+    old = torch.randn(rows, dim, generator=g, device="cuda").to(T[gt])
+    ids = make_ids(n, rows, torch.int64 if seed % 2 else torch.int32, seed, kind)
+    got = run_grad(dout, ids, -1.25, old, MODE[mode], seed=seed * 977, base=seed % 1000)
+    check_grad(dout, ids, -1.25, old, got, MODE[mode], gt)
+
+
 @pytest.mark.parametrize("n", [2, 31, 32, 33, 63, 64, 65, 95, 96, 97, 128, 129, 160, 1000, 2048, 2049, 4096, 4097,
                                8192, 8193, 16384, 20000,
-                               32768, 32769, 70000])
+                               32768, 32769, 70000, 140000])
 @pytest.mark.parametrize("kind", ["one", "zipf", "mixed", "runs"])
 def test_grad_run_lengths(n, kind):
     """Runs that end at, before and after every chunk border, both sorts, and
