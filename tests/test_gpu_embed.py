@@ -88,6 +88,26 @@ def test_lookup(table, out, rows, dim, n):
         assert intact()
 
 
+@pytest.mark.parametrize("out", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("table", ["int8", "fp32", "bf16", "fp16"])
+def test_lookup_every_remainder(table, out):
+    """Widths of every remainder: groups that start at any element, last groups
+    of every length."""
+    g = torch.Generator().manual_seed(5)
+    ids = make_ids(37, 9, torch.int64, 6)
+    for dim in list(range(1, 18)) + list(range(505, 522)):
+        res, intact = guarded((37, dim), T[out])
+        if table == "int8":
+            codes = torch.randint(-128, 128, (9, dim), generator=g, dtype=torch.int8)
+            scales = torch.rand(-(-9 * dim // 32), generator=g)
+            w = torch.from_numpy(O.dequant_int8(codes.numpy().reshape(-1), scales.numpy(), 32)).view(9, dim)
+            zq.zq_embed_lookup_int8(codes.cuda(), scales.cuda(), 32, ids.cuda(), 1.5, res)
+        else:
+            w = torch.randn(9, dim, generator=g).to(T[table])
+            zq.zq_embed_lookup(w.cuda(), ids.cuda(), 1.5, res)
+        assert same(res, expect_lookup(w.float(), ids, 1.5, T[out])) and intact(), dim
+
+
 def test_lookup_special_values():
     """Infinities, NaN, signed zeros, subnormals and results past fp16's range."""
     v = torch.tensor([math.inf, -math.inf, math.nan, 0.0, -0.0, 1e-42, -3e-39, 1e30, 70000.0, 65519.0, 1e-8, 6e-8])
@@ -199,6 +219,18 @@ def test_grad_of_many_tokens(mode, gt, n, rows, dim):
     ids = make_ids(n, rows, torch.int64, n)
     got = run_grad(dout, ids, 0.3, old, MODE[mode], seed=n, base=dim)
     check_grad(dout, ids, 0.3, old, got, MODE[mode], gt)
+
+
+@pytest.mark.parametrize("mode,gt", MODES)
+@pytest.mark.parametrize("dt", ["fp32", "bf16", "fp16"])
+def test_grad_every_remainder(mode, gt, dt):
+    g = torch.Generator(device="cuda").manual_seed(7)
+    ids = make_ids(150, 11, torch.int32, 8)
+    for dim in list(range(1, 18)) + list(range(509, 522)):
+        dout = torch.randn(150, dim, generator=g, device="cuda").to(T[dt])
+        old = torch.randn(11, dim, generator=g, device="cuda").to(T[gt])
+        got = run_grad(dout, ids, 0.7, old, MODE[mode], seed=dim, base=3 * dim)
+        check_grad(dout, ids, 0.7, old, got, MODE[mode], gt)
 
 
 SWEEP = np.random.default_rng(2024)

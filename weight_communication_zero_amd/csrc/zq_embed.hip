@@ -69,6 +69,8 @@ __global__ __launch_bounds__(kBlockThreads) void lookup_kernel(LookupArgs a) {
 #pragma unroll
         for (int u = 0; u < kLookU; ++u) {
             float x[G];
+            if constexpr (!WHOLE)
+                whole<IN, G>(v[u], (uint32_t)a.dim - col[u]);
             widen<IN, G>(v[u], x);
             if constexpr (IN == kQ8) {
                 const uint64_t e = row[u] * a.dim + col[u];

@@ -516,11 +516,14 @@ __device__ __forceinline__ RowBits<T, OUT> load_row(const void* __restrict__ p, 
     return r;
 }
 
-template <int T, int OUT>
-__device__ __forceinline__ void widen_row(const RowBits<T, OUT>& r, float x[8]) {
+template <int T, int OUT, bool WHOLE>
+__device__ __forceinline__ void widen_row(RowBits<T, OUT> r, const Cols<OUT>& c, float x[8]) {
 #pragma unroll
-    for (int h = 0; h < Cols<OUT>::H; ++h)
+    for (int h = 0; h < Cols<OUT>::H; ++h) {
+        if constexpr (!WHOLE)
+            whole<T, Cols<OUT>::G>(r.h[h], c.left[h]);
         widen<T, Cols<OUT>::G>(r.h[h], x + h * Cols<OUT>::G);
+    }
 }
 
 // A long run's partial sums.
@@ -557,7 +560,7 @@ __device__ __forceinline__ void finish(const SumArgs& a, const float s[8],
         g[j] = a.scale * s[j];
     if constexpr (MODE != kGradWrite) {
         float o[8];
-        widen_row<OUT, OUT>(old, o);
+        widen_row<OUT, OUT, WHOLE>(old, c, o);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             g[j] = o[j] + g[j];
@@ -617,7 +620,7 @@ struct Window {
                 if (p + u >= e)
                     break;
                 float v[8];
-                widen_row<IN, OUT>(x[u], v);
+                widen_row<IN, OUT, WHOLE>(x[u], cols, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     s[j] += v[j];
