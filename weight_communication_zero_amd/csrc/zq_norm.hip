@@ -34,7 +34,9 @@ constexpr uint32_t kClipMaxWgs = 1u << 24;
 // 249.4 / 262.5 / 248.9 us with 1024 / 2048 / 4096 of them (6.8 TB/s; a fill
 // writes 6.9), and with plain loads in place of nontemporal ones 274.
 constexpr uint32_t kNormMaxWgs = 4096;
-constexpr uint32_t kNormOneWg = 64;  // most tiles that one workgroup sums by itself
+// Most tiles that one workgroup sums by itself, in one launch: 16 / 64 / 128 tiles
+// take 2.7 / 4.2 / 6.4 us in a graph so, and 4.1 / 4.3 / 4.4 us as sum and join.
+constexpr uint32_t kNormOneWg = 64;
 
 // A tile is 64 lanes x U 16-byte vectors.
 template <int T, int U>
