@@ -41,7 +41,7 @@ constexpr uint64_t kRangeTokens = 1 << 15;
 constexpr uint64_t kRangeRows = 1 << 20;
 constexpr uint64_t kRangeWork = 1ull << 32;  // tokens times rows
 constexpr uint32_t kRangeBins = 512;  // most rows a workgroup takes
-constexpr uint32_t kRangeWgs = 64;
+constexpr uint32_t kRangeWgs = 64;    // where the rows ask for no more; 32 to 256 are alike
 constexpr uint32_t kRangeThreads = 1024;
 
 // Sort by digits.
@@ -52,8 +52,7 @@ constexpr uint32_t kSortItems = 4;
 constexpr uint32_t kSortRound = kSortThreads * kSortItems;
 constexpr uint32_t kSortBlocks = 256;
 
-
-constexpr uint32_t kJoinThreads = 512;
+constexpr uint32_t kJoinThreads = 512;  // 256 and 1024 took 0 to 2 us more a call
 // A workgroup clears rows of about this size together, with nontemporal stores:
 // 16384 tokens into fp32 [32000, 2048] took 70.2 / 71.7 / 73.1 us with 8 / 16 /
 // 32 KB, and 80.4 with plain stores.
@@ -612,8 +611,7 @@ struct Window {
                 x[u] = load_row<IN, OUT, WHOLE, dout_nt<IN, OUT>()>(a.dout, t, a.dim, cols);
                 if constexpr (MODE != kGradWrite)
                     if (((ends >> q) & 1) && q != long_end)
-                        old[u] = load_row<OUT, OUT, WHOLE, false>(a.grad, key_at(q),
-                                                                                a.dim, cols);
+                        old[u] = load_row<OUT, OUT, WHOLE, false>(a.grad, key_at(q), a.dim, cols);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -705,7 +703,8 @@ __device__ __forceinline__ void clear_rows(const SumArgs& a, uint32_t j) {
     const Raw<OUT, G> zero = {};
     while (row < rows) {
         if (!((named >> row) & 1))
-            store_group<OUT, G, WHOLE, true>(zero, a.grad, (uint64_t)(r0 + row) * a.dim + (uint64_t)group * G,
+            store_group<OUT, G, WHOLE, true>(zero, a.grad,
+                                             (uint64_t)(r0 + row) * a.dim + (uint64_t)group * G,
                                              (uint32_t)a.dim - group * G);
         row += row_step;
         group += group_step;
@@ -929,7 +928,8 @@ hipError_t grad_t(const EmbedGradArgs& a, hipStream_t st) {
 
 template <int IN, int OUT, int MODE>
 hipError_t grad_m(const EmbedGradArgs& a, hipStream_t st) {
-    return a.dim % Cols<OUT>::G == 0 ? grad_t<IN, OUT, MODE, true>(a, st) : grad_t<IN, OUT, MODE, false>(a, st);
+    return a.dim % Cols<OUT>::G == 0 ? grad_t<IN, OUT, MODE, true>(a, st)
+                                     : grad_t<IN, OUT, MODE, false>(a, st);
 }
 
 template <int IN, int OUT>
