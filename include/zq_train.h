@@ -88,7 +88,8 @@ zq_status zq_embed_lookup_int8(const int8_t *codes, const float *scales, uint32_
  *                    are neither read nor written;
  *   ZQ_GRAD_ADD_SR:  the same rounded as zq_sr_accumulate rounds, with
  *                    element v * dim + j at index counter_base + v * dim + j
- *                    of the random stream of `seed` (bf16 only).
+ *                    of the random stream of `seed` (bf16 only).  The seed is
+ *                    part of the call, so a graph replays the same numbers.
  * The sum runs in binary32 over the tokens in ascending t, in groups whose
  * borders depend on the ids alone: equal inputs give equal bits.  No atomic
  * operation touches a sum.
@@ -155,8 +156,9 @@ size_t zq_grad_sumsq_workspace(uint32_t n_seg);
  * zq_grad_clip_batched -- clipping by the global norm:
  *   norm = sqrt(*sumsq);  c = min(1, max_norm / (norm + eps))   (binary64,
  *   c rounded once to binary32);  out_i = fl(c * g_i) rounded to g_dtype.
- * A NaN in *sumsq gives c = NaN; an infinity gives c = 0.  Where c == 1 and
- * out is g itself, the tensor is neither read nor written.
+ * A NaN in *sumsq gives c = NaN, as does 0 / 0 (max_norm, eps and the norm all
+ * 0); an infinity gives c = 0.  Where c == 1 and out is g itself, the tensor is
+ * neither read nor written.
  *
  *   segs   HOST array of n_seg segments (read during the call only).
  *   sumsq  one binary64 on the device, read only.

@@ -64,6 +64,8 @@ LISTS = {
     "empty": [], "zero": [0, 0], "one": [1], "odd": [3, 0, 17, 1023, 1024, 1025], "tile": [2047, 2048, 2049, 4096],
     "one_wg": [1024 * 64], "past_one_wg": [1024 * 64 + 1], "one_wg_16bit": [2048 * 64, 0], "past_16bit": [2048 * 64, 1],
     "128_segments": [65] * 128, "129_segments": [65] * 129, "300_segments": list(range(300)),
+    "144_segments": [70] * 144, "145_segments": [70] * 145, "192_segments": [9] * 192, "193_segments": [9] * 193,
+    "400_with_empty": [0, 33] * 200,
     "mid": [100003, 7, 65536, 99999, 1], "large_first": [3_000_001, 5, 9],
 }
 
@@ -103,7 +105,8 @@ def test_sumsq_of_infinities_and_nan(at):
 @pytest.mark.parametrize("in_place", [True, False])
 @pytest.mark.parametrize("max_norm,eps", [(0.5, 1e-6), (1e9, 1e-6), (0.0, 1e-6), (0.1, 0.0), (1e-30, 0.5)])
 @pytest.mark.parametrize("dt", list(T))
-@pytest.mark.parametrize("name", ["one", "odd", "tile", "129_segments", "300_segments", "mid"])
+@pytest.mark.parametrize("name", ["one", "odd", "tile", "129_segments", "144_segments", "145_segments",
+                                  "300_segments", "400_with_empty", "mid"])
 def test_clip(name, dt, max_norm, eps, in_place):
     ts = tensors(LISTS[name], T[dt], 3, std=1.0)
     bufs = [torch.cat([t.cuda(), torch.full((GUARD,), 7.0, dtype=t.dtype, device="cuda")]) for t in ts]
