@@ -334,6 +334,21 @@ def test_quant_dequant_int8(block, wdt):
             assert_bits_equal(out.host(), o_o, what + f" dequant to {odt}")
 
 
+@pytest.mark.parametrize("odt,tdt", [("fp32", torch.float32), ("bf16", torch.bfloat16), ("fp16", torch.float16)])
+@pytest.mark.parametrize("n", [8192, 1001])
+def test_dequant_int8_signs_of_zero(n, odt, tdt):
+    """Codes and scales of any origin: a negative code times a scale of 0 (or a
+    positive one times -0) is -0, and stays -0 in every output type; products
+    that round to zero keep their sign."""
+    codes = np.random.default_rng(n).integers(-128, 128, size=n).astype(np.int8)
+    scales = np.resize(np.array([0.0, -0.0, 1e-10, -1e-45, 1e-3], np.float32), -(-n // 32))
+    exp = O.dequant_int8(codes, scales, 32, out_bf16=odt == "bf16", out_f16=odt == "fp16")
+    out = Guarded(n, tdt)
+    Z().zq_dequant_int8(to_gpu(codes), to_gpu(scales), 32, out.t)
+    torch.cuda.synchronize()
+    assert_bits_equal(out.host(), exp, f"dequant to {odt}")
+
+
 # ------------------------------------------------------ stochastic rounding --
 
 def sr_inputs(n, seed, special=False):

@@ -81,8 +81,8 @@ __device__ __forceinline__ float half_hi(uint32_t w) {
         return f16hi(w);
 }
 
-// Two fp32 -> packed bf16 pair, round to nearest even (gfx950 v_cvt_pk_bf16_f32).
-// Only used on finite values.
+// Two fp32 -> packed bf16 pair, round to nearest even (gfx950 v_cvt_pk_bf16_f32;
+// infinities stay, NaN gives a quiet NaN).
 __device__ __forceinline__ uint32_t pack_bf16_rne(float lo, float hi) {
     typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
     bf2 v = {(__bf16)lo, (__bf16)hi};
@@ -96,6 +96,14 @@ __device__ __forceinline__ uint32_t pack_f16_rne(float lo, float hi) {
     typedef _Float16 h2 __attribute__((ext_vector_type(2)));
     h2 v = {(_Float16)lo, (_Float16)hi};
     return __builtin_bit_cast(uint32_t, v);
+}
+
+// A binary32 product about to be rounded to fp16, kept apart from the rounding:
+// the compiler may otherwise join the two into one v_fma_mixlo_f16 with a +0
+// addend, which turns a product of -0 into +0.
+__device__ __forceinline__ float apart(float x) {
+    asm("" : "+v"(x));
+    return x;
 }
 
 template <int T>

@@ -211,14 +211,6 @@ __device__ __forceinline__ void widen(const Raw<T, G>& r, float* x) {
     }
 }
 
-// A binary32 product about to be rounded to fp16, kept apart from the rounding:
-// the compiler otherwise joins the two into one v_fma_mixlo_f16 with a +0
-// addend, which turns a product of -0 into +0.
-__device__ __forceinline__ float apart(float x) {
-    asm("" : "+v"(x));
-    return x;
-}
-
 // Two fp32 products in type T's bits, rounded to nearest even.
 template <int T>
 __device__ __forceinline__ uint32_t pack_products(float lo, float hi) {
