@@ -161,6 +161,67 @@ def test_binding_refuses_a_segment_table_used_with_other_sizes():
         zq.zq_quantize_ef_int4_batched(efq, 256, 1.0, 1.0, stream=0)
 
 
+class TensorOn:
+    """What the binding asks of a GPU tensor, with a fake, misaligned address
+    (so that the C ABI refuses every call that gets as far)."""
+    is_cuda = True
+
+    def __init__(self, device, dtype, numel, at=FAKE + 4):
+        self._device, self.dtype, self._numel, self._at = device, dtype, numel, at
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self._numel
+
+    def get_device(self):
+        return self._device
+
+    def data_ptr(self):
+        return self._at
+
+
+@pytest.mark.parametrize("kind", ["sr", "efq", "dr", "sumsq", "clip"])
+def test_binding_refuses_a_segment_table_used_on_another_device(monkeypatch, kind):
+    """A marshalled table's tensors were found to be on the device that was
+    current then; with another device current, the kernels would run there on
+    the first one's memory."""
+    import torch
+    on = lambda d, t, n=4096: TensorOn(d, t, n)
+    bf, f, u8, f64 = torch.bfloat16, torch.float32, torch.uint8, torch.float64
+    monkeypatch.setattr(zq, "_device", lambda: 0)
+    if kind == "sr":
+        table = zq.SrSegmentTable([(on(0, bf), on(0, bf), 64, 0, 1, 0)])
+        call = lambda: zq.zq_sr_accumulate_batched(table, stream=0)
+    elif kind == "efq":
+        table = zq.EfqSegmentTable([(on(0, f), None, on(0, u8), on(0, f))], 128)
+        call = lambda: zq.zq_quantize_ef_int4_batched(table, 128, 1.0, 1.0, stream=0)
+    elif kind == "dr":  # raw pointers beside a tensor
+        table = zq.DrSegmentTable([(FAKE + 4, FAKE + 4, 4096, 2048, 32, on(0, f), None, None, None)], 1, 128)
+        call = lambda: zq.zq_dequant_reduce_batched(table, 1, 128, 1.0, stream=0)
+    else:
+        table = zq.GradSegmentTable([(on(0, f), on(0, f))])
+        now = lambda t, n: on(zq._device(), t, n)
+        if kind == "sumsq":
+            call = lambda: zq.zq_grad_sumsq_batched(table, now(f64, 1), now(u8, table.workspace), stream=0)
+        else:
+            call = lambda: zq.zq_grad_clip_batched(table, now(f64, 1), 1.0, stream=0)
+    with pytest.raises(zq.ZQError, match="ALIGN"):  # the same device: the C ABI's own checks run
+        call()
+    monkeypatch.setattr(zq, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:0, the current device is cuda:1"):
+        call()
+
+
+def test_segment_tables_of_raw_pointers_name_no_device():
+    odd = FAKE + 4
+    sr = zq.SrSegmentTable([(odd, odd + 0x100000, 64, 0, 1, 0)])
+    with pytest.raises(zq.ZQError, match="ALIGN"):
+        zq.zq_sr_accumulate_batched(sr, stream=0)
+    assert zq.zq_sr_accumulate_batched(zq.SrSegmentTable([]), stream=0) is None
+
+
 def test_sr_batched_validation():
     Seg = zq.SrSegment
 

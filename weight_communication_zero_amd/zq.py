@@ -302,7 +302,22 @@ def zq_sr_accumulate(dst, src, seed: int, counter_base: int = 0, zero_src: bool 
                                 _stream(stream)))
 
 
-class SrSegmentTable:
+class _SegmentTable:
+    """What the marshalled tables share: the device of their tensors, which
+    _need has found to be the current one (None: raw pointers only)."""
+    device = None
+
+    def note_device(self) -> None:
+        self.device = next((t.get_device() for seg in self.segments for t in seg
+                            if hasattr(t, "get_device")), None)
+
+    def check_device(self) -> None:
+        if self.device is not None and self.device != _device():
+            raise ValueError(f"the segment table's tensors are on cuda:{self.device}, the current "
+                             f"device is cuda:{_device()}")
+
+
+class SrSegmentTable(_SegmentTable):
     """A marshalled segment table for zq_sr_accumulate_batched: build it once
     for a fixed set of buffers and pass it to every call (the tensors are
     kept alive by the table)."""
@@ -316,6 +331,7 @@ class SrSegmentTable:
             src_len = src.numel() if not isinstance(src, int) else off + n
             self.arr[i] = SrSegment(_p(dst), _p(src), n, off, src_len, seed, cb)
         self.ptr = C.cast(self.arr, C.c_void_p)
+        self.note_device()
 
 
 def zq_sr_accumulate_batched(segments, zero_src: bool = False, stream=None) -> None:
@@ -325,12 +341,13 @@ def zq_sr_accumulate_batched(segments, zero_src: bool = False, stream=None) -> N
     which elements [src_offset, src_offset + n) are added into dst[0:n]; with
     zero_src every element of every src buffer is cleared in the same pass."""
     table = segments if isinstance(segments, SrSegmentTable) else SrSegmentTable(segments)
+    table.check_device()
     _check("zq_sr_accumulate_batched",
            lib.zq_sr_accumulate_batched(table.ptr, len(table.segments), 1 if zero_src else 0,
                                         _stream(stream)))
 
 
-class EfqSegmentTable:
+class EfqSegmentTable(_SegmentTable):
     """A marshalled segment table for zq_quantize_ef_int4_batched: tuples
     (g, ef or None, codes, scales) of per-tensor buffers (n = g.numel())."""
 
@@ -351,6 +368,7 @@ class EfqSegmentTable:
             self.arr[i] = EfqSegment(_p(g), _p(ef), _p(codes), _p(scales), n)
         self.block = block
         self.ptr = C.cast(self.arr, C.c_void_p)
+        self.note_device()
 
 
 def zq_quantize_ef_int4_batched(segments, block: int, beta_e: float, beta_r: float,
@@ -358,6 +376,7 @@ def zq_quantize_ef_int4_batched(segments, block: int, beta_e: float, beta_r: flo
     """Per-tensor EF int4 quantize of many tensors in one call: `segments` is
     an EfqSegmentTable or an iterable of (g, ef or None, codes, scales)."""
     table = segments if isinstance(segments, EfqSegmentTable) else EfqSegmentTable(segments, block)
+    table.check_device()
     if table.block != block:
         raise ValueError(f"the segment table was checked for block {table.block}, not {block}")
     _check("zq_quantize_ef_int4_batched",
@@ -366,7 +385,7 @@ def zq_quantize_ef_int4_batched(segments, block: int, beta_e: float, beta_r: flo
                                            beta_e, beta_r, _stream(stream)))
 
 
-class DrSegmentTable:
+class DrSegmentTable(_SegmentTable):
     """A marshalled segment table for zq_dequant_reduce_batched.  Each
     segment is (codes, scales, n, codes_stride, scales_stride, out, rq_codes,
     rq_scales, rq_ef): codes a uint8 tensor holding the P peer chunks (peer q
@@ -388,6 +407,7 @@ class DrSegmentTable:
                                     _p(rqe))
         self.P, self.block = P, block
         self.ptr = C.cast(self.arr, C.c_void_p)
+        self.note_device()
 
 
 def zq_dequant_reduce_batched(segments, P: int, block: int, alpha: float, rq_beta_e: float = 0.0,
@@ -395,6 +415,7 @@ def zq_dequant_reduce_batched(segments, P: int, block: int, alpha: float, rq_bet
     """Per-tensor dequantize-reduce(-requant) of many tensors in one call:
     `segments` is a DrSegmentTable or an iterable of its tuples."""
     table = segments if isinstance(segments, DrSegmentTable) else DrSegmentTable(segments, P, block)
+    table.check_device()
     if (table.P, table.block) != (P, block):
         raise ValueError(f"the segment table was checked for P={table.P}, block={table.block}, "
                          f"not P={P}, block={block}")
@@ -469,7 +490,7 @@ def zq_embed_grad(dout, ids, scale: float, grad, mode: int, workspace, seed: int
                              workspace.numel() if workspace is not None else 0, _stream(stream)))
 
 
-class GradSegmentTable:
+class GradSegmentTable(_SegmentTable):
     """A marshalled segment table for zq_grad_sumsq_batched and
     zq_grad_clip_batched: pairs (g, out) of gradient tensors of one dtype,
     where out is g itself, another buffer of g's size, or None (only the sum of
@@ -489,6 +510,7 @@ class GradSegmentTable:
             self.arr[i] = GradSegment(_p(g), _p(out), n)
         self.workspace = grad_sumsq_workspace(len(self.segments))
         self.ptr = C.cast(self.arr, C.c_void_p)
+        self.note_device()
 
 
 def grad_sumsq_workspace(n_seg: int) -> int:
@@ -502,6 +524,7 @@ def zq_grad_sumsq_batched(segments, sumsq, workspace, accumulate: bool = False,
     `segments`: a GradSegmentTable or an iterable of (g, out or None);
     workspace: a uint8 tensor of grad_sumsq_workspace(n_seg) bytes."""
     table = segments if isinstance(segments, GradSegmentTable) else GradSegmentTable(segments)
+    table.check_device()
     _need("sumsq", sumsq, 1, _F64)
     _need("workspace", workspace, table.workspace, _U8)
     _check("zq_grad_sumsq_batched",
@@ -517,6 +540,7 @@ def zq_grad_clip_batched(segments, sumsq, max_norm: float, eps: float = 1e-6, no
     """out = g * min(1, max_norm / (sqrt(sumsq) + eps)) for every segment;
     norm (one float32, optional) gets sqrt(sumsq)."""
     table = segments if isinstance(segments, GradSegmentTable) else GradSegmentTable(segments)
+    table.check_device()
     _need("sumsq", sumsq, 1, _F64)
     _need("norm", norm, 1, _F32)
     _check("zq_grad_clip_batched",
