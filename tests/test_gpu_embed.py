@@ -279,6 +279,27 @@ def test_grad_run_lengths(n, kind):
     assert torch.equal(got.cpu(), exp)
 
 
+@pytest.mark.parametrize("n,dim", [(64, 16), (65, 16), (300, 8), (5000, 520), (24000, 16), (40000, 1544), (300000, 16),
+                                   (1 << 20, 16)])
+@pytest.mark.parametrize("other", [0, 10])
+def test_grad_error_of_long_runs(n, dim, other):
+    """The header's bound for a row of m tokens, min(m - 1, 70 + m / 64) u / (1 -
+    that u) times the sum of |dout| with u = 2^-24 (the write is exact with scale
+    1), on positive values, whose partial sums are as large as they get; one row
+    has all the tokens, or all but `other` % of them."""
+    g = torch.Generator(device="cuda").manual_seed(n + other)
+    rows = 5
+    dout = torch.rand(n, dim, generator=g, device="cuda").add_(0.5)
+    ids = torch.full((n,), 3, device="cuda")
+    ids[torch.rand(n, generator=g, device="cuda") * 100 < other] = 1
+    got = run_grad(dout, ids, 1.0, torch.zeros(rows, dim), zq.ZQ_GRAD_WRITE).double()
+    for r in (1, 3):
+        m = int((ids == r).sum())
+        exact = dout[ids == r].double().sum(0)
+        ku = min(max(m - 1, 0), 70 + m // 64) * 2.0 ** -24
+        assert bool(((got[r] - exact).abs() <= ku / (1 - ku) * exact).all())
+
+
 @pytest.mark.parametrize("rows", [1, 2, 255, 511, 512, 513, 50257, 262143, 262144, 300001, 500003, 2 ** 20,
                                   2 ** 27 + 5])
 @pytest.mark.parametrize("n", [300, 9000])
