@@ -22,6 +22,8 @@
  *     lookup gives it a row of zeros and the gradient leaves the token out,
  *     so padding may carry any such id (-1, say).
  *   - Inputs may hold infinities and NaN; results follow from the formulas.
+ * zq_abi_version() counts the calls of zq.h alone; a program that loads the
+ * library at run time looks up the names below to see whether it has them.
  */
 #ifndef ZQ_TRAIN_H
 #define ZQ_TRAIN_H

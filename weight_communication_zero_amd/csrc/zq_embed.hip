@@ -9,9 +9,10 @@
 // lane its own from there.  G is 4 where an element has four bytes on either
 // side, so that every access covers whole lines, else 8.
 //
-// 16384 tokens x 4096 from int8 codes into bf16 take 26.5 us, 157 MB at 5.9 TB/s
-// (41 us with plain in place of nontemporal stores: the output then displaces
-// the rows that are read again); 8192 x 768 from fp32 6.6 us; one token 2.5 us.
+// 16384 tokens x 4096 from int8 codes into bf16 take 26 us in most bursts of
+// calls, 157 MB at 6.0 TB/s, and up to 32 in others on the same inputs (41 us
+// with plain in place of nontemporal stores: the output then displaces the rows
+// that are read again); 8192 x 768 from fp32 6.7 us; one token 2.3 us.
 #include "zq_rows.h"
 
 namespace zq {

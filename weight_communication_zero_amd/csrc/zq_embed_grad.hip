@@ -18,10 +18,13 @@
 // only count.
 //
 // Bound by memory where there is much of it: 32768 bf16 tokens x 4096 added into
-// fp32 move 557 MB in the sum's 119 us (4.7 TB/s, a copy's rate); counters show no
-// byte twice but the partials'.  Around it the sort takes 15 us and the join 8;
-// with 8192 tokens x 768 the three launches take 6 + 11 + 5 us, each little more
-// than its start and one chain of dependent reads.
+// fp32 move 557 MB in the sum's 120 us (4.7 TB/s, a copy's rate); counters show no
+// byte twice but the partials'.  Around it the sort takes 15 us and the join 9;
+// with 8192 tokens x 768 the three launches take 6 + 12 + 5 us.  The sum there is
+// 2048 waves, half of which have only 32 lanes with columns.
+// A row that most tokens name is slow: one workgroup sorts its tokens and one per
+// 512 columns joins its partials (32768 bf16 tokens x 768 added into fp32 take
+// 113 us when all name one row, 47 with text's ids).
 #include <algorithm>
 
 #include "zq_rows.h"
@@ -33,10 +36,10 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr uint32_t kCols = kWave * 8;
 
 // Sort by ranges: its workgroups, one for every kRangeBins rows at least, each
-// read all the tokens.  A whole gradient call (16 columns) took, by ranges / by
-// digits: 32768 tokens 31.8 / 37.7 us with 2^17 rows, 40.9 / 37.7 with 2^18; 8192
+// read all the tokens.  A whole gradient call (bf16 added into 16 fp32 columns,
+// ids drawn evenly) took, by ranges / by digits: 32768 tokens 31.8 / 37.7 us with 2^17 rows, 40.9 / 37.7 with 2^18; 8192
 // tokens 29.1 / 36.9 with 2^19, 45.4 / 37.4 with 2^20; 2048 tokens 25.0 / 31.2
-// with 2^20; and 65536 tokens into [32000, 1024] 87.5 / 79.0.
+// with 2^20; and 65536 bf16 tokens written into fp32 [32000, 1024] 87.5 / 79.0.
 constexpr uint64_t kRangeTokens = 1 << 15;
 constexpr uint64_t kRangeRows = 1 << 20;
 constexpr uint64_t kRangeWork = 1ull << 32;  // tokens times rows
@@ -72,7 +75,7 @@ constexpr uint32_t sum_threads() {
 // long ones leave fewer partials of long runs.  With 4096 / 8192 / 16384 waves
 // wanted, 16384 tokens written into fp32 [32000, 2048] took 67.5 / 70.4 / 70.4
 // us, 32768 added into [32000, 4096] 144.4 / 144.4 / 148.8, 200000 added into
-// [32000, 1024] 176 / 176 / 196.
+// [32000, 1024] 176 / 176 / 196 (bf16 tokens in all three).
 constexpr uint64_t kWantWaves = 4096;
 uint32_t chunk_tokens(uint64_t n_tok, uint64_t col_tiles) {
     for (uint32_t c = 32; c > 8; c /= 2)
@@ -327,7 +330,10 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortArgs a) {
 
 // Sort by digits: a stable counting sort, least significant digit first, over
 // at most kSortBlocks workgroups.  Counts one digit of a workgroup's tokens; the
-// first digit's launch also clears the row flags, which the last one sets.
+// first digit's launch also clears the row flags, which the last one sets.  The
+// number of tokens alone sets the grid, so few tokens clear the flags of many
+// rows slowly: 64 tokens written into fp32 [2^20, 16] take 30 us (by ranges),
+// into [2^20 + 1, 16] 102, into [2^22, 16] 338.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
     __shared__ uint32_t cnt[kBins];
     const uint32_t t = threadIdx.x;

@@ -9,10 +9,14 @@
 // workgroup, the workgroups' partials in a fixed order) depends on the
 // segments' sizes alone, so equal inputs give equal bits.  No atomics.
 //
-// Both are bound by memory.  The sum reads 4 / 2 B/elem: 0.85 G elements in 492 us
+// Both are bound by memory.  The sum reads 4 / 2 B/elem: 0.85 G elements in 494 us
 // (fp32) or 246 (bf16), 6.9 TB/s.  The clip reads and writes them: 1071 us in
-// fp32, 6.4 TB/s.  Small lists are bound by the launches: 29 MB of fp16 in 111
-// tensors take 8 + 2.5 us (sum and join) and 13 us (clip).
+// fp32, 6.35 TB/s, 1074 in place.  28 MB of fp16 in 111 ragged tensors take 8 + 2
+// us (sum and join) and 12 us (clip, a copy's rate).  A ragged last tile goes
+// element by element; with every tensor filled up to whole tiles the three take
+// 0.8 us and 0.7 us less.
+// A clip in place with c = 1 touches no tensor, but the grid is the same: 0.85 G
+// fp32 elements are 1.6 million workgroups, which come and go in 352 us.
 #include <algorithm>
 
 #include "zq_rows.h"

@@ -1,11 +1,11 @@
 """ctypes binding of libzq (include/zq.h, include/zq_train.h): argument marshalling only.
 
-Every function takes torch tensors (device memory) or raw integer device
-pointers, converts them to the C ABI's plain pointers and sizes, passes the
-current torch HIP stream unless one is given, and raises ``ZQError`` on a
-non-OK status.  All arithmetic happens in libzq's HIP kernels; there is no
-fallback path: if ``libzq.so`` is missing or cannot be loaded, importing this
-module fails.
+Every function takes torch tensors (device memory) or, where it reads no size
+or element type off the argument, raw integer device pointers, converts them to
+the C ABI's plain pointers and sizes, passes the current torch HIP stream unless
+one is given, and raises ``ZQError`` on a non-OK status.  All arithmetic happens
+in libzq's HIP kernels; there is no fallback path: if ``libzq.so`` is missing or
+cannot be loaded, importing this module fails.
 """
 from __future__ import annotations
 
