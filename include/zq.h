@@ -18,6 +18,8 @@
  *
  * zq_train.h continues this ABI (same library, same conventions) with the two
  * ends of the step: embedding lookup and gradient, gradient norm and clipping.
+ * zq_layers.h continues it with what lies between them: SwiGLU and linear
+ * gradients from int8 activations, and the vocabulary projection's cross entropy.
  *
  * Conventions shared by every compute entry point
  *   - Buffers are DEVICE pointers on the current HIP device unless stated.

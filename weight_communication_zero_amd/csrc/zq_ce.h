@@ -1,0 +1,194 @@
+// zq_ce.h -- what the cross entropy's loss and gradient share: the tokens that
+// count, gathered; the plan of a call's workspace; pieces of the projection.
+#pragma once
+
+#include "zq_mm_plan.h"
+#include "zq_stage.h"
+
+namespace zq {
+
+// Scalars in the workspace.
+struct CeScalars {
+    uint32_t count;    // tokens that count
+    float up, down;    // the power of two that scales q, and its inverse
+};
+
+// The tokens that count, in order: r-th of them is token list[r].
+struct CeTokens {
+    CeScalars* scalars;
+    uint32_t* list;
+    uint32_t* target;
+    float *lse, *dloss;  // gradient only
+};
+
+struct CePrepArgs {
+    const void* ids;
+    uint32_t id64, n_tok, rows, scaled;
+    const float *lse, *dloss;
+    float *loss, *lse_out;  // loss only: cleared where a token is left out
+    CeTokens t;
+};
+
+// Gathers the tokens that count.  One workgroup: 2^14 tokens take two rounds (of
+// 8192 ids, 8 a thread, in flight together), and positions need no second pass.
+static __global__ __launch_bounds__(1024) void ce_prep_kernel(CePrepArgs a) {
+    __shared__ uint32_t sums[16], maxima[16];
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t count = 0, top = 0;
+    for (uint32_t base = 0; base < a.n_tok; base += 8192) {
+        const uint32_t first = base + wave * 512 + lane;
+        uint64_t id[8];
+        load_ids<8>(a.ids, a.id64, [&](int j) { return min(first + j * 64, a.n_tok - 1); }, id);
+        uint64_t there[8];
+        uint32_t mine = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            there[j] = __builtin_amdgcn_ballot_w64(first + j * 64 < a.n_tok && id[j] < a.rows);
+            mine += (uint32_t)__builtin_popcountll(there[j]);
+        }
+        if (lane == 0)
+            sums[wave] = mine;
+        __syncthreads();
+        uint32_t at = count;
+#pragma unroll
+        for (uint32_t w = 0; w < 16; ++w) {
+            at += w < wave ? sums[w] : 0;
+            count += sums[w];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t t = first + j * 64;
+            const uint32_t r = at + (uint32_t)__builtin_popcountll(
+                                        there[j] & (((uint64_t)1 << lane) - 1));
+            at += (uint32_t)__builtin_popcountll(there[j]);
+            if (there[j] >> lane & 1) {
+                a.t.list[r] = t;
+                a.t.target[r] = (uint32_t)id[j];
+                if (a.dloss) {
+                    const float g = a.dloss[t];
+                    a.t.lse[r] = a.lse[t];
+                    a.t.dloss[r] = g;
+                    top = max(top, absbits(g) < 0x7F800000u ? absbits(g) : 0);
+                }
+            } else if (a.loss && t < a.n_tok) {
+                a.loss[t] = 0.0f;
+                a.lse_out[t] = 0.0f;
+            }
+        }
+    }
+    top = group_max<64>(top);
+    if (lane == 0)
+        maxima[wave] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < 16; ++w)
+            top = max(top, maxima[w]);
+        // 2^(14 - exponent): exponents of a power of two and of its inverse stay normal.
+        int shift = 0;
+        if (a.scaled && top)
+            shift = min(max(141 - (int)(top >> 23), -120), 120);
+        a.t.scalars->count = count;
+        a.t.scalars->up = bitsf((uint32_t)(127 + shift) << 23);
+        a.t.scalars->down = bitsf((uint32_t)(127 - shift) << 23);
+    }
+}
+
+// Byte offsets in the workspace.
+struct CeLayout {
+    uint64_t kp;              // width of staged rows: dim up to a multiple of 64
+    uint32_t piece, n_pieces;
+    MmPlan logits;
+    uint64_t scalars, list, target, lse, dloss, x, w;
+    uint64_t part, run, z_target;   // loss
+    uint64_t q, acc, sums;          // gradient
+    uint64_t ldacc;
+    uint64_t total;
+
+    uint32_t rows_of(uint32_t i, uint32_t rows) const {
+        return i + 1 < n_pieces ? piece : rows - i * piece;
+    }
+};
+
+struct CeTake {
+    uint64_t at = 0;
+    uint64_t operator()(uint64_t bytes) {
+        const uint64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    }
+};
+
+// Pieces of `rows` of at most `most` rows each (multiples of 256), of one size but
+// for the last.
+inline void ce_pieces(CeLayout& l, uint32_t rows, uint64_t most) {
+    most = std::max<uint64_t>(std::min<uint64_t>(most, (uint64_t)1 << 22) / 256 * 256, 256);
+    l.n_pieces = (uint32_t)div_up(rows, most);
+    l.piece = (uint32_t)round_up(div_up(rows, l.n_pieces), 256);
+    l.n_pieces = (uint32_t)div_up(rows, l.piece);
+}
+
+inline void ce_take_tokens(CeLayout& l, CeTake& take, uint32_t n_tok, bool grad) {
+    l.scalars = take(sizeof(CeScalars));
+    l.list = take((uint64_t)n_tok * 4);
+    l.target = take((uint64_t)n_tok * 4);
+    l.lse = take(grad ? (uint64_t)n_tok * 4 : 0);
+    l.dloss = take(grad ? (uint64_t)n_tok * 4 : 0);
+    l.x = take(n_tok * l.kp * 2);
+    l.w = take(l.piece * l.kp * 2);
+}
+
+inline CeTokens ce_tokens(const CeLayout& l, char* ws) {
+    return {(CeScalars*)(ws + l.scalars), (uint32_t*)(ws + l.list), (uint32_t*)(ws + l.target),
+            (float*)(ws + l.lse), (float*)(ws + l.dloss)};
+}
+
+inline hipError_t ce_prep(const CeArgs& a, const CeTokens& t, bool scaled, hipStream_t stream) {
+    CePrepArgs p = {a.ids, a.id64, a.n_tok, a.rows, scaled, a.lse, a.dloss, a.loss, a.lse_out, t};
+    void* args[] = {&p};
+    return hipLaunchKernel((const void*)&ce_prep_kernel, dim3(1), dim3(1024), args, 0, stream);
+}
+
+// The hidden states of the tokens that count.
+template <int T>
+hipError_t ce_stage_x(const CeArgs& a, const CeLayout& l, const CeTokens& t, char* ws,
+                      hipStream_t stream) {
+    StageArgs s = {};
+    s.src = a.x;
+    s.dim = a.dim;
+    s.rows = a.n_tok;
+    s.ld = (uint32_t)l.kp;
+    s.out = (uint16_t*)(ws + l.x);
+    s.list = t.list;
+    s.count = &t.scalars->count;
+    return launch_stage<T>(s, T, stream);
+}
+
+// Rows v0 .. v0 + n - 1 of the projection as an operand: where they lie, or (codes,
+// widths that are no multiple of 64) staged.
+template <int T>
+hipError_t ce_piece(const CeArgs& a, int w_type, const CeLayout& l, uint32_t v0, uint32_t n,
+                    char* ws, MmOperand* op, hipStream_t stream) {
+    if (w_type != kQ8 && a.dim % kMmK == 0) {
+        *op = {(const uint16_t*)a.w + (uint64_t)v0 * a.dim, a.dim};
+        return hipSuccess;
+    }
+    StageArgs s = {};
+    s.src = a.w;
+    s.scales = a.w_scales;
+    s.log2b = a.log2b;
+    s.dim = a.dim;
+    s.row0 = v0;
+    s.rows = n;
+    s.ld = (uint32_t)l.kp;
+    s.out = (uint16_t*)(ws + l.w);
+    *op = {s.out, l.kp};
+    return launch_stage<T>(s, w_type == kQ8 ? kQ8 : T, stream);
+}
+
+// exp(x), off by about (1 + |x|) 2^-24 of itself.
+__device__ __forceinline__ float exp_of(float x) {
+    return __builtin_amdgcn_exp2f(x * 0x1.715476p0f);
+}
+
+}  // namespace zq

@@ -1,0 +1,205 @@
+// zq_ce_grad.hip -- the gradient of the vocabulary projection's cross entropy.
+//
+// For each piece of the vocabulary three products on one tile engine:
+//   q  = dloss (exp(scale x w^T - lse) - [target])   rounded to 16 bits, in the
+//        workspace: tokens x piece
+//   dx += q w        (kept in binary32 between pieces)
+//   dw  = q^T x      (this piece's rows, whole)
+// The second and third take their operands as they lie, by transposed reads from
+// LDS, so nothing is stored transposed.
+#include "zq_ce.h"
+
+namespace zq {
+namespace {
+
+struct Residual {
+    struct Args {
+        float scale;
+        uint16_t* q;
+        uint64_t ldq;
+        CeTokens t;
+        uint32_t v0;
+    };
+
+    template <class S>
+    static __device__ __forceinline__ void finish(const Args& e, f4 (&acc)[S::MI][S::NI],
+                                                  uint32_t M, uint32_t N, uint32_t m0, uint32_t n0,
+                                                  uint32_t wm, uint32_t wn, uint32_t lane,
+                                                  unsigned char*) {
+        const float up = e.t.scalars->up;
+        const uint32_t nw = n0 + wn * (S::BN / S::WN) + (lane >> 4) * 4;
+        const uint32_t end = (N + kMmK - 1) / kMmK * kMmK;  // zeros up to here
+#pragma unroll
+        for (int i = 0; i < S::MI; ++i) {
+            const uint32_t m = m0 + wm * (S::BM / S::WM) + i * 16 + (lane & 15);
+            if (m >= M)
+                continue;
+            const uint32_t target = e.t.target[m] - e.v0;
+            const float lse = e.t.lse[m], g = e.t.dloss[m] * up;
+#pragma unroll
+            for (int j = 0; j < S::NI; ++j) {
+                const uint32_t n = nw + j * 16;
+                float q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float p = exp_of(e.scale * acc[i][j][k] - lse);
+                    q[k] = g * (n + k == target ? p - 1.0f : p);
+                    q[k] = n + k < N ? q[k] : 0.0f;
+                }
+                if (n < end)
+                    *(u2*)(e.q + m * e.ldq + n) =
+                        u2{pack_half_rne<S::T>(q[0], q[1]), pack_half_rne<S::T>(q[2], q[3])};
+            }
+        }
+    }
+};
+
+struct LeftOutArgs {
+    const void* ids;
+    uint32_t id64, n_tok, rows, dim;
+    uint16_t* dx;
+};
+
+// Clears the rows of dx whose tokens are left out: a wave a token.
+__global__ __launch_bounds__(256) void left_out_kernel(LeftOutArgs a) {
+    for (uint32_t t = (uint32_t)wave_id(); t < a.n_tok; t += (uint32_t)wave_count()) {
+        uint64_t id[1];
+        load_ids<1>(a.ids, a.id64, [&](int) { return t; }, id);
+        if (id[0] < a.rows)
+            continue;
+        uint16_t* row = a.dx + (uint64_t)t * a.dim;
+        for (uint32_t j = (uint32_t)lane_id(); j < a.dim; j += kWave)
+            row[j] = 0;
+    }
+}
+
+CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
+    CeLayout l = {};
+    l.kp = round_up(dim, kMmK);
+    const uint64_t n_pad = round_up(n_tok, 256);
+    // The library's choice: 512 MiB of q and of staged rows.
+    uint64_t most = piece ? round_up(std::min<uint64_t>(piece, rows), 256)
+                          : ((uint64_t)1 << 28) / std::max(n_pad, l.kp);
+    most = std::min(most, ((uint64_t)1 << 36) / std::max(n_pad, l.kp));
+    ce_pieces(l, rows, most);
+    l.logits = mm_plan(n_tok, l.piece, l.kp, false);
+    CeTake take;
+    ce_take_tokens(l, take, n_tok, true);
+    l.q = take((uint64_t)n_tok * l.piece * 2);
+    l.ldacc = round_up(dim, 4);
+    l.acc = take(l.n_pieces > 1 ? n_tok * l.ldacc * 4 : 0);
+    uint64_t floats = 0;
+    for (uint32_t n : {l.piece, l.rows_of(l.n_pieces - 1, rows)}) {
+        floats = std::max(floats, part_floats(mm_plan(n_tok, dim, n, true), n_tok, dim));
+        floats = std::max(floats, part_floats(mm_plan(n, dim, n_tok, true), n, dim));
+    }
+    l.sums = take(floats * 4);
+    l.total = take.at;
+    return l;
+}
+
+template <int T>
+hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_t stream) {
+    const CeLayout l = layout(a.n_tok, a.rows, a.dim, a.piece);
+    char* ws = (char*)a.workspace;
+    const CeTokens tok = ce_tokens(l, ws);
+    hipError_t st = ce_prep(a, tok, T == kF16, stream);
+    if (st == hipSuccess)
+        st = ce_stage_x<T>(a, l, tok, ws, stream);
+    if (st == hipSuccess && a.dx) {
+        LeftOutArgs o = {a.ids, a.id64, a.n_tok, a.rows, a.dim, (uint16_t*)a.dx};
+        void* args[] = {&o};
+        st = hipLaunchKernel((const void*)&left_out_kernel,
+                             dim3(std::min<uint32_t>((a.n_tok + 3) / 4, 4096)), dim3(256), args, 0,
+                             stream);
+    }
+    const MmOperand x = {(const uint16_t*)(ws + l.x), l.kp};
+    const MmOperand q = {(const uint16_t*)(ws + l.q), l.piece};
+    float* acc = (float*)(ws + l.acc);
+    float* sums = (float*)(ws + l.sums);
+    const uint32_t* count = &tok.scalars->count;
+    for (uint32_t i = 0; i < l.n_pieces && st == hipSuccess; ++i) {
+        const uint32_t v0 = i * l.piece, n = l.rows_of(i, a.rows);
+        MmOperand w;
+        st = ce_piece<T>(a, w_type, l, v0, n, ws, &w, stream);
+        if (st != hipSuccess)
+            break;
+        MmArgs m = {};
+        m.a = x;
+        m.b = w;
+        m.M = a.n_tok;
+        m.N = n;
+        m.K = (uint32_t)l.kp;
+        m.dyn_m = count;
+        Residual::Args e = {a.scale, (uint16_t*)(ws + l.q), l.piece, tok, v0};
+        st = launch_mm<T, false, false, Residual>(m, e, l.logits, stream);
+        MmOut o = {};
+        o.ldacc = l.ldacc;
+        o.ldo = a.dim;
+        o.factor = &tok.scalars->down;
+        o.scale = a.scale;
+        if (st == hipSuccess && a.dx) {
+            m.a = q;
+            m.N = a.dim;
+            m.K = n;
+            m.b_cols = (uint32_t)l.kp;
+            MmOut d = o;
+            d.acc_in = i ? acc : nullptr;
+            d.acc_out = i + 1 < l.n_pieces ? acc : nullptr;
+            d.out = a.dx;
+            d.list = tok.list;
+            d.type = T;
+            st = launch_mm_sum<T, false, true>(m, d, mm_plan(a.n_tok, a.dim, n, true), sums,
+                                               stream);
+        }
+        if (st == hipSuccess && a.dw) {
+            MmArgs g = {};
+            g.a = q;
+            g.b = x;
+            g.M = n;
+            g.N = a.dim;
+            g.K = a.n_tok;
+            g.a_cols = l.piece;
+            g.b_cols = (uint32_t)l.kp;
+            g.dyn_k = count;
+            MmOut d = o;
+            d.out = (char*)a.dw + (uint64_t)v0 * a.dim * (dw_type == kF32 ? 4 : 2);
+            d.type = dw_type;
+            d.add = mode == kGradAdd;
+            st = launch_mm_sum<T, true, true>(g, d, mm_plan(n, a.dim, a.n_tok, true), sums, stream);
+        }
+    }
+    return st;
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(uint32_t* p, uint64_t words, uint32_t rest) {
+    const uint64_t first = blockIdx.x * 256ull + threadIdx.x;
+    for (uint64_t i = first; i < words; i += gridDim.x * 256ull)
+        p[i] = 0;
+    if (first < rest)
+        ((uint8_t*)(p + words))[first] = 0;
+}
+
+}  // namespace
+
+hipError_t launch_clear(void* p, uint64_t bytes, hipStream_t stream) {
+    uint32_t* q = (uint32_t*)p;
+    uint64_t words = bytes / 4;
+    uint32_t rest = bytes % 4;
+    void* args[] = {&q, &words, &rest};
+    const uint64_t wgs = std::min<uint64_t>(words / 256 + 1, 16384);
+    return hipLaunchKernel((const void*)&clear_kernel, dim3((uint32_t)wgs), dim3(256), args, 0,
+                           stream);
+}
+
+size_t ce_grad_workspace(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
+    return layout(n_tok, rows, dim, piece).total;
+}
+
+hipError_t launch_ce_grad(const CeArgs& a, int type, int w_type, int dw_type, int mode,
+                          hipStream_t stream) {
+    return type == kBF16 ? launch<kBF16>(a, w_type, dw_type, mode, stream)
+                         : launch<kF16>(a, w_type, dw_type, mode, stream);
+}
+
+}  // namespace zq

@@ -1,0 +1,94 @@
+// zq_mm_plan.h -- host side of the matrix products: which tile a product takes,
+// into how many parts its k's are split, and the launches.
+#pragma once
+
+#include <algorithm>
+
+#include "zq_mm.h"
+
+namespace zq {
+
+// The tiles there are: 256 x 256 by 8 waves (128 KiB of LDS, one workgroup a
+// CU), 128 x 128 by 4 waves (64 KiB, two a CU).
+enum MmTileKind : int { kTile256 = 0, kTile128 = 1 };
+
+struct MmPlan {
+    int kind;
+    uint32_t splits;
+};
+
+constexpr uint32_t kMaxSplits = 32;
+
+constexpr uint32_t tile_edge(int kind) { return kind == kTile256 ? 256 : 128; }
+
+inline uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+inline uint64_t round_up(uint64_t a, uint64_t b) { return div_up(a, b) * b; }
+
+// Floats of partial sums that a plan needs.
+inline uint64_t part_floats(const MmPlan& p, uint64_t M, uint64_t N) {
+    return p.splits > 1 ? p.splits * M * round_up(N, 4) : 0;
+}
+
+// The tile and the splits of the least time by a simple model: rounds of
+// workgroups over the CUs, each of its steps (with all CUs at work a step of 64 k's
+// takes 1.8 us for a 256-tile and 1.0 us for a 128-tile, two of which share a CU) and
+// of 3 us around them; and for a split the partial sums' way to memory and back.
+inline MmPlan mm_plan(uint64_t M, uint64_t N, uint64_t K, bool may_split) {
+    const uint64_t steps = std::max<uint64_t>(div_up(K, kMmK), 1);
+    MmPlan best = {kTile256, 1};
+    double least = 1e30;
+    for (int kind : {kTile256, kTile128}) {
+        const uint64_t e = tile_edge(kind), tiles = div_up(M, e) * div_up(N, e);
+        const uint64_t slots = kind == kTile256 ? 256 : 512;
+        const double step_us = kind == kTile256 ? 1.8 : 1.0;
+        for (uint64_t s = 1; s <= (may_split ? kMaxSplits : 1) && (s == 1 || steps / s >= 4); ++s) {
+            const double rounds = (double)div_up(tiles * s, slots);
+            double us = rounds * ((double)div_up(steps, s) * step_us + 3.0);
+            if (s > 1)
+                us += 3.0 + (double)(2 * s * M * N) * 4 / 4e6;
+            if (us < least) {
+                least = us;
+                best = {kind, (uint32_t)s};
+            }
+        }
+    }
+    return best;
+}
+
+template <class S, class Epi>
+hipError_t launch_mm_shape(const MmArgs& a, const typename Epi::Args& e, uint32_t splits,
+                           hipStream_t stream) {
+    const uint64_t tiles = div_up(a.M, S::BM) * div_up(a.N, S::BN);
+    MmArgs k = a;
+    typename Epi::Args ke = e;
+    void* args[] = {&k, &ke};
+    return hipLaunchKernel((const void*)&mm_kernel<S, Epi>,
+                           dim3((uint32_t)div_up(tiles, 8) * 8, splits), dim3(S::kThreads), args, 0,
+                           stream);
+}
+
+template <int T, bool TA, bool TB, class Epi>
+hipError_t launch_mm(const MmArgs& a, const typename Epi::Args& e, const MmPlan& p,
+                     hipStream_t stream) {
+    if (p.kind == kTile256)
+        return launch_mm_shape<MmShape<T, 256, 256, 2, 4, 2, TA, TB>, Epi>(a, e, p.splits, stream);
+    return launch_mm_shape<MmShape<T, 128, 128, 2, 2, 2, TA, TB>, Epi>(a, e, p.splits, stream);
+}
+
+// A product into MmOut, its partial sums (where split) in `part`.
+template <int T, bool TA, bool TB>
+hipError_t launch_mm_sum(const MmArgs& a, const MmOut& o, const MmPlan& p, float* part,
+                         hipStream_t stream) {
+    MmSum::Args e = {o, p.splits > 1 ? part : nullptr, a.M, round_up(a.N, 4)};
+    hipError_t st = launch_mm<T, TA, TB, MmSum>(a, e, p, stream);
+    if (st != hipSuccess || p.splits == 1)
+        return st;
+    uint32_t splits = p.splits, M = a.M, N = a.N;
+    const uint32_t* dyn = a.dyn_m;
+    void* args[] = {&e, &splits, &M, &N, &dyn};
+    const uint64_t wgs = std::min<uint64_t>(div_up((uint64_t)M * div_up(N, 4), 256), 8192);
+    return hipLaunchKernel((const void*)&mm_join_kernel, dim3((uint32_t)wgs), dim3(256), args, 0,
+                           stream);
+}
+
+}  // namespace zq

@@ -1,0 +1,77 @@
+// zq_stage.h -- operands of the matrix products laid out in a call's workspace:
+// rows of 16-bit values of the product's type with zeros up to a padded width, from
+// rows of any width or from qwZ codes, all rows or those of a list.
+#pragma once
+
+#include "zq_layers_launch.h"
+#include "zq_rows.h"
+
+namespace zq {
+
+struct StageArgs {
+    const void* src;        // values or codes, rows of `dim` elements
+    const float* scales;
+    uint32_t log2b;
+    uint64_t dim, row0;     // the first row taken
+    uint32_t rows, ld;      // rows and width of the result, a multiple of 8
+    uint16_t* out;
+    const uint32_t* list;   // row r is src's row list[r], for r < *count
+    const uint32_t* count;
+};
+
+// A lane per group of 8 elements of the result.
+template <int T, int IN, bool WHOLE>
+__global__ __launch_bounds__(256) void stage_kernel(StageArgs a) {
+    const uint32_t rows = a.count ? min(a.rows, *a.count) : a.rows;
+    const uint32_t per_row = a.ld / 8;
+    const uint64_t groups = (uint64_t)rows * per_row;
+    for (uint64_t g = blockIdx.x * 256ull + threadIdx.x; g < groups; g += gridDim.x * 256ull) {
+        const uint32_t r = (uint32_t)(g / per_row);
+        const uint32_t c = (uint32_t)(g - (uint64_t)r * per_row) * 8;
+        Raw<T, 8> v = {{0, 0, 0, 0}};
+        if (c < a.dim) {
+            const uint64_t e = ((a.list ? a.list[r] : r) + a.row0) * a.dim + c;
+            const uint32_t left = (uint32_t)(a.dim - c);
+            Raw<IN, 8> x = load_group<IN, 8, WHOLE, false>(a.src, e, left);
+            if constexpr (!WHOLE)
+                whole<IN, 8>(x, left);
+            if constexpr (IN == kQ8) {
+                // A group touches two blocks at most (a block has 32 elements or more).
+                const uint64_t last = e + (left < 8 ? left : 8) - 1;
+                const float s0 = a.scales[e >> a.log2b];
+                const float s1 = WHOLE ? s0 : a.scales[last >> a.log2b];
+                float y[8];
+                widen<IN, 8>(x, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y[j] = j < (int)left ? y[j] * ((e + j) >> a.log2b == e >> a.log2b ? s0 : s1)
+                                         : 0.0f;
+                v = narrow<T, 8>(y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v.w[i] = x.w[i];
+            }
+        }
+        store_group<T, 8, true, false>(v, a.out, g * 8, 8);
+    }
+}
+
+// in: T, or kQ8.
+template <int T>
+hipError_t launch_stage(const StageArgs& a, int in, hipStream_t stream) {
+    if (a.rows == 0)
+        return hipSuccess;
+    const bool whole = a.dim % 8 == 0;
+    const void* fn = in == kQ8 ? whole ? (const void*)&stage_kernel<T, kQ8, true>
+                                       : (const void*)&stage_kernel<T, kQ8, false>
+                     : whole   ? (const void*)&stage_kernel<T, T, true>
+                               : (const void*)&stage_kernel<T, T, false>;
+    StageArgs k = a;
+    void* args[] = {&k};
+    const uint64_t wgs = ((uint64_t)a.rows * (a.ld / 8) + 255) / 256;
+    return hipLaunchKernel(fn, dim3((uint32_t)(wgs < 65536 ? wgs : 65536)), dim3(256), args, 0,
+                           stream);
+}
+
+}  // namespace zq

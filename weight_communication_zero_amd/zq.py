@@ -1,4 +1,4 @@
-"""ctypes binding of libzq (include/zq.h, include/zq_train.h): argument marshalling only.
+"""ctypes binding of libzq (include/zq.h, zq_train.h, zq_layers.h): argument marshalling only.
 
 Every function takes torch tensors (device memory) or, where it reads no size
 or element type off the argument, raw integer device pointers, converts them to
@@ -108,6 +108,24 @@ def _load() -> C.CDLL:
     L.zq_embed_grad_workspace.restype = sz
     L.zq_grad_sumsq_workspace.argtypes = [u32]
     L.zq_grad_sumsq_workspace.restype = sz
+    L.zq_swiglu_int8.argtypes = [vp, vp, i32, sz, u32, vp, vp, vp, vp, vp, vp]
+    L.zq_swiglu_grad_int8.argtypes = [vp, vp, vp, vp, u32, vp, i32, sz, vp, vp, vp, vp]
+    L.zq_linear_grad_int8.argtypes = [vp, i32, vp, vp, u32, sz, u64, u64, vp, i32, i32, vp, sz, vp]
+    L.zq_ce_loss.argtypes = [vp, i32, sz, u64, vp, u64, vp, i32, f32, vp, vp, u64, vp, sz, vp]
+    L.zq_ce_loss_int8.argtypes = [vp, i32, sz, u64, vp, vp, u32, u64, vp, i32, f32, vp, vp, u64, vp,
+                                  sz, vp]
+    L.zq_ce_grad.argtypes = [vp, i32, sz, u64, vp, u64, vp, i32, f32, vp, vp, vp, vp, i32, i32, u64,
+                             vp, sz, vp]
+    L.zq_ce_grad_int8.argtypes = [vp, i32, sz, u64, vp, vp, u32, u64, vp, i32, f32, vp, vp, vp, vp,
+                                  i32, i32, u64, vp, sz, vp]
+    for f in ("zq_swiglu_int8", "zq_swiglu_grad_int8", "zq_linear_grad_int8", "zq_ce_loss",
+              "zq_ce_loss_int8", "zq_ce_grad", "zq_ce_grad_int8"):
+        getattr(L, f).restype = i32
+    L.zq_linear_grad_workspace.argtypes = [sz, u64, u64]
+    L.zq_ce_loss_workspace.argtypes = [sz, u64, u64, u64]
+    L.zq_ce_grad_workspace.argtypes = [sz, u64, u64, u64]
+    for f in ("zq_linear_grad_workspace", "zq_ce_loss_workspace", "zq_ce_grad_workspace"):
+        getattr(L, f).restype = sz
     L.zq_abi_version.argtypes = []
     L.zq_abi_version.restype = u32
     return L
@@ -191,6 +209,7 @@ _U8 = (torch.uint8,)
 _I8 = (torch.int8,)
 _F64 = (torch.float64,)
 _INDEX = (torch.int32, torch.int64)
+_HALF = (torch.bfloat16, torch.float16)
 
 
 def _check(fn: str, st: int) -> None:
@@ -547,3 +566,157 @@ def zq_grad_clip_batched(segments, sumsq, max_norm: float, eps: float = 1e-6, no
            lib.zq_grad_clip_batched(table.ptr, len(table.segments),
                                     ZQ_FP32 if table.dtype is None else table.dtype, _p(sumsq),
                                     max_norm, eps, _p(norm), _stream(stream)))
+
+
+def _blocks(n: int, block: int) -> int:
+    return (n + block - 1) // block if block > 0 else 0
+
+
+def zq_swiglu_int8(gate, up, block: int, h, gate_codes, gate_scales, up_codes, up_scales,
+                   stream=None) -> None:
+    """h = gate * sigmoid(gate) * up (fp32/bf16/fp16, all of one dtype), and gate
+    and up as zq_quant_int8 blocks for zq_swiglu_grad_int8."""
+    n = gate.numel()
+    _need("gate", gate, n, _FLOAT)
+    _need("up", up, n, (gate.dtype,))
+    _need("h", h, n, (gate.dtype,))
+    _need("gate_codes", gate_codes, n, _I8)
+    _need("gate_scales", gate_scales, _blocks(n, block), _F32)
+    _need("up_codes", up_codes, n, _I8)
+    _need("up_scales", up_scales, _blocks(n, block), _F32)
+    _check("zq_swiglu_int8",
+           lib.zq_swiglu_int8(_p(gate), _p(up), _dtype(gate), n, block, _p(h), _p(gate_codes),
+                              _p(gate_scales), _p(up_codes), _p(up_scales), _stream(stream)))
+
+
+def zq_swiglu_grad_int8(gate_codes, gate_scales, up_codes, up_scales, block: int, dh, dgate, dup,
+                        h=None, stream=None) -> None:
+    """dgate and dup of zq_swiglu_int8 at its kept values, for h's gradient dh
+    (fp32/bf16/fp16, all of one dtype); h, where given, gets the product of the
+    kept values."""
+    n = dh.numel()
+    _need("gate_codes", gate_codes, n, _I8)
+    _need("gate_scales", gate_scales, _blocks(n, block), _F32)
+    _need("up_codes", up_codes, n, _I8)
+    _need("up_scales", up_scales, _blocks(n, block), _F32)
+    _need("dh", dh, n, _FLOAT)
+    _need("dgate", dgate, n, (dh.dtype,))
+    _need("dup", dup, n, (dh.dtype,))
+    _need("h", h, n, (dh.dtype,))
+    _check("zq_swiglu_grad_int8",
+           lib.zq_swiglu_grad_int8(_p(gate_codes), _p(gate_scales), _p(up_codes), _p(up_scales),
+                                   block, _p(dh), _dtype(dh), n, _p(dgate), _p(dup), _p(h),
+                                   _stream(stream)))
+
+
+def linear_grad_workspace(n_tok: int, out_dim: int, in_dim: int) -> int:
+    """Bytes of workspace zq_linear_grad_int8 needs."""
+    return lib.zq_linear_grad_workspace(n_tok, out_dim, in_dim)
+
+
+def _bytes(workspace) -> int:
+    return workspace.numel() if workspace is not None else 0
+
+
+def zq_linear_grad_int8(dy, codes, scales, block: int, grad, mode: int, workspace,
+                        stream=None) -> None:
+    """grad [out, in] (=, with ZQ_GRAD_ADD +=) dy^T x for dy [tokens, out] (bf16/fp16)
+    and the layer's input x [tokens, in] kept as zq_quant_int8 blocks; grad
+    fp32/bf16/fp16.  workspace: a uint8 tensor of linear_grad_workspace(tokens, out,
+    in) bytes, one for each call that may run at the same time."""
+    out_dim, in_dim = _rows_dim("grad", grad)
+    n_tok, dy_dim = _rows_dim("dy", dy)
+    if dy_dim != out_dim:
+        raise ValueError(f"dy has {dy_dim} columns, grad {out_dim} rows")
+    _need("dy", dy, n_tok * out_dim, _HALF)
+    _need("codes", codes, n_tok * in_dim, _I8)
+    _need("scales", scales, _blocks(n_tok * in_dim, block), _F32)
+    _need("grad", grad, out_dim * in_dim, _FLOAT)
+    _need("workspace", workspace, linear_grad_workspace(n_tok, out_dim, in_dim), _U8)
+    _check("zq_linear_grad_int8",
+           lib.zq_linear_grad_int8(_p(dy), _dtype(dy), _p(codes), _p(scales), block, n_tok, out_dim,
+                                   in_dim, _p(grad), _dtype(grad), mode, _p(workspace),
+                                   _bytes(workspace), _stream(stream)))
+
+
+def ce_loss_workspace(n_tok: int, rows: int, dim: int, piece: int = 0) -> int:
+    """Bytes of workspace zq_ce_loss and zq_ce_loss_int8 need."""
+    return lib.zq_ce_loss_workspace(n_tok, rows, dim, piece)
+
+
+def ce_grad_workspace(n_tok: int, rows: int, dim: int, piece: int = 0) -> int:
+    """Bytes of workspace zq_ce_grad and zq_ce_grad_int8 need."""
+    return lib.zq_ce_grad_workspace(n_tok, rows, dim, piece)
+
+
+def _ce_loss(fn, x, w, w_args, rows: int, dim: int, ids, scale, loss, lse, workspace, piece,
+             stream) -> None:
+    n = ids.numel()
+    _need("x", x, n * dim, _HALF)
+    _need("ids", ids, n, _INDEX)
+    _need("loss", loss, n, _F32)
+    _need("lse", lse, n, _F32)
+    _need("workspace", workspace, ce_loss_workspace(n, rows, dim, piece), _U8)
+    _check(fn, getattr(lib, fn)(_p(x), _dtype(x), n, dim, _p(w), *w_args, rows, _p(ids),
+                                _index(ids), scale, _p(loss), _p(lse), piece, _p(workspace),
+                                _bytes(workspace), _stream(stream)))
+
+
+def zq_ce_loss(x, w, ids, scale: float, loss, lse, workspace, piece: int = 0, stream=None) -> None:
+    """Per-token softmax cross entropy of the logits scale * x w^T, which are never
+    kept: x (ids.numel() * dim) and w [rows, dim] bf16 or fp16, ids int32/int64 (one
+    outside the vocabulary leaves its token out: loss and lse 0), loss and lse fp32.
+    workspace: a uint8 tensor of ce_loss_workspace(tokens, rows, dim, piece) bytes;
+    piece: vocabulary rows worked on at a time (0: the library's choice)."""
+    rows, dim = _rows_dim("w", w)
+    _need("w", w, rows * dim, (x.dtype,))
+    _ce_loss("zq_ce_loss", x, w, (), rows, dim, ids, scale, loss, lse, workspace, piece, stream)
+
+
+def zq_ce_loss_int8(x, codes, scales, block: int, ids, scale: float, loss, lse, workspace,
+                    piece: int = 0, stream=None) -> None:
+    """zq_ce_loss with the projection in qwZ's form: codes [rows, dim] int8 and
+    scales fp32, as zq_quant_int8 writes them for the flat matrix."""
+    rows, dim = _rows_dim("codes", codes)
+    _need("codes", codes, rows * dim, _I8)
+    _need("scales", scales, _blocks(rows * dim, block), _F32)
+    _ce_loss("zq_ce_loss_int8", x, codes, (_p(scales), block), rows, dim, ids, scale, loss, lse,
+             workspace, piece, stream)
+
+
+def _ce_grad(fn, x, w, w_args, rows: int, dim: int, ids, scale, lse, dloss, dx, dw, mode, workspace,
+             piece, stream) -> None:
+    n = ids.numel()
+    _need("x", x, n * dim, _HALF)
+    _need("ids", ids, n, _INDEX)
+    _need("lse", lse, n, _F32)
+    _need("dloss", dloss, n, _F32)
+    _need("dx", dx, n * dim, (x.dtype,))
+    _need("dw", dw, rows * dim, _FLOAT)
+    _need("workspace", workspace, ce_grad_workspace(n, rows, dim, piece), _U8)
+    _check(fn, getattr(lib, fn)(_p(x), _dtype(x), n, dim, _p(w), *w_args, rows, _p(ids),
+                                _index(ids), scale, _p(lse), _p(dloss), _p(dx), _p(dw),
+                                ZQ_FP32 if dw is None else _dtype(dw), mode, piece, _p(workspace),
+                                _bytes(workspace), _stream(stream)))
+
+
+def zq_ce_grad(x, w, ids, scale: float, lse, dloss, dx, dw, mode: int, workspace, piece: int = 0,
+               stream=None) -> None:
+    """The gradient of zq_ce_loss for the losses' gradients dloss (fp32, a token
+    each): dx like x, dw [rows, dim] fp32/bf16/fp16 written (ZQ_GRAD_WRITE) or added
+    to (ZQ_GRAD_ADD); dx or dw may be None.  lse is what zq_ce_loss wrote.  workspace:
+    a uint8 tensor of ce_grad_workspace(tokens, rows, dim, piece) bytes."""
+    rows, dim = _rows_dim("w", w)
+    _need("w", w, rows * dim, (x.dtype,))
+    _ce_grad("zq_ce_grad", x, w, (), rows, dim, ids, scale, lse, dloss, dx, dw, mode, workspace,
+             piece, stream)
+
+
+def zq_ce_grad_int8(x, codes, scales, block: int, ids, scale: float, lse, dloss, dx, dw, mode: int,
+                    workspace, piece: int = 0, stream=None) -> None:
+    """zq_ce_grad with the projection in qwZ's form (see zq_ce_loss_int8)."""
+    rows, dim = _rows_dim("codes", codes)
+    _need("codes", codes, rows * dim, _I8)
+    _need("scales", scales, _blocks(rows * dim, block), _F32)
+    _ce_grad("zq_ce_grad_int8", x, codes, (_p(scales), block), rows, dim, ids, scale, lse, dloss,
+             dx, dw, mode, workspace, piece, stream)
