@@ -21,36 +21,46 @@ struct Residual {
         uint32_t v0;
     };
 
+    // A token's target in the piece, its lse, and its scaled loss gradient.
+    struct Row {
+        uint32_t target;
+        float lse, g;
+    };
+    static __device__ __forceinline__ Row row(const Args& e, uint32_t M, uint32_t m0,
+                                              uint32_t tid) {
+        const uint32_t m = min(m0 + tid, M - 1);
+        return {e.t.target[m] - e.v0, e.t.lse[m], e.t.dloss[m] * e.t.scalars->up};
+    }
+
     template <class S>
-    static __device__ __forceinline__ void finish(const Args& e, f4 (&acc)[S::MI][S::NI],
-                                                  uint32_t M, uint32_t N, uint32_t m0, uint32_t n0,
-                                                  uint32_t wm, uint32_t wn, uint32_t lane,
-                                                  unsigned char*) {
-        const float up = e.t.scalars->up;
-        const uint32_t nw = n0 + wn * (S::BN / S::WN) + (lane >> 4) * 4;
-        const uint32_t end = (N + kMmK - 1) / kMmK * kMmK;  // zeros up to here
-#pragma unroll
-        for (int i = 0; i < S::MI; ++i) {
-            const uint32_t m = m0 + wm * (S::BM / S::WM) + i * 16 + (lane & 15);
-            if (m >= M)
-                continue;
-            const uint32_t target = e.t.target[m] - e.v0;
-            const float lse = e.t.lse[m], g = e.t.dloss[m] * up;
-#pragma unroll
-            for (int j = 0; j < S::NI; ++j) {
-                const uint32_t n = nw + j * 16;
+    static __device__ __forceinline__ void finish(const Args& e, const Row& mine,
+                                                  f4 (&acc)[S::MI][S::NI], uint32_t M, uint32_t N,
+                                                  uint32_t m0, uint32_t n0, uint32_t wm,
+                                                  uint32_t wn, uint32_t lane, unsigned char* lds) {
+        // The rows' values behind the part of LDS that the sums go through.
+        static_assert(S::kThreads >= S::BM && S::kRowsLds + S::BM * sizeof(Row) <= S::kLds, "fits");
+        Row* rows = (Row*)(lds + S::kRowsLds);
+        if (threadIdx.x < S::BM)
+            rows[threadIdx.x] = mine;
+        __syncthreads();
+        const uint32_t end = (N + kMmK - 1) / kMmK * kMmK;  // zeros from N up to here
+        mm_rows<S>(
+            acc, wm, wn, lane, lds, [](uint32_t, uint32_t) { return f4{0, 0, 0, 0}; },
+            [&](uint32_t r, uint32_t c, f4 z, f4) {
+                const uint32_t m = m0 + r, n = n0 + c;
+                if (m >= M || n >= end)
+                    return;
+                const Row t = rows[r];
                 float q[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float p = exp_of(e.scale * acc[i][j][k] - lse);
-                    q[k] = g * (n + k == target ? p - 1.0f : p);
+                    const float p = exp_of(e.scale * z[k] - t.lse);
+                    q[k] = t.g * (n + k == t.target ? p - 1.0f : p);
                     q[k] = n + k < N ? q[k] : 0.0f;
                 }
-                if (n < end)
-                    *(u2*)(e.q + m * e.ldq + n) =
-                        u2{pack_half_rne<S::T>(q[0], q[1]), pack_half_rne<S::T>(q[2], q[3])};
-            }
-        }
+                *(u2*)(e.q + m * e.ldq + n) =
+                    u2{pack_half_rne<S::T>(q[0], q[1]), pack_half_rne<S::T>(q[2], q[3])};
+            });
     }
 };
 

@@ -33,11 +33,16 @@ struct Stats {
         float* z_target;
     };
 
+    using Row = MmNoRow;
+    static __device__ __forceinline__ Row row(const Args&, uint32_t, uint32_t, uint32_t) {
+        return {};
+    }
+
     template <class S>
-    static __device__ __forceinline__ void finish(const Args& e, f4 (&acc)[S::MI][S::NI],
-                                                  uint32_t M, uint32_t N, uint32_t m0, uint32_t n0,
-                                                  uint32_t wm, uint32_t wn, uint32_t lane,
-                                                  unsigned char* lds) {
+    static __device__ __forceinline__ void finish(const Args& e, const Row&,
+                                                  f4 (&acc)[S::MI][S::NI], uint32_t M, uint32_t N,
+                                                  uint32_t m0, uint32_t n0, uint32_t wm,
+                                                  uint32_t wn, uint32_t lane, unsigned char* lds) {
         f2* pair = (f2*)lds;  // [WN][BM]
         const uint32_t nw = n0 + wn * (S::BN / S::WN) + (lane >> 4) * 4;
 #pragma unroll

@@ -26,6 +26,8 @@ struct MmArgs {
     MmOperand a, b;
     uint32_t M, N, K;
     uint32_t a_cols, b_cols;   // of a transposed operand: stored columns (a multiple of 8)
+    const uint32_t* a_rows;    // where set, row m of a plain a is stored row a_rows[m]
+                               // (all of them within 4 GiB)
     const uint32_t* dyn_m;     // where set, M (K) is the smaller of M (K) and this
     const uint32_t* dyn_k;
 };
@@ -72,11 +74,6 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
     }
 }
 
-__device__ __forceinline__ h4 lds_read_tr(uint32_t at) {
-    typedef __attribute__((address_space(3))) h4 lds_h4;
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_h4*)(uintptr_t)at);
-}
-
 // The LDS side of one operand of ROWS rows.  Stored by 16-byte chunks so that
 // the reads below meet no bank twice:
 //   plain       row r, chunk c of 8 at (r, c ^ (r & 7))
@@ -88,41 +85,48 @@ struct MmTile {
     static_assert(kLoads * WAVES * 1024 == kBytes, "whole loads");
 
     uint32_t voff[kLoads];
-    uint32_t klane[TR ? kLoads : 1], coff[TR ? kLoads : 1];
 
-    // rows: rows (plain) or columns (transposed) there are from the tile's first on.
-    __device__ __forceinline__ void init(uint32_t wave, uint32_t lane, uint64_t ld, uint32_t rows) {
+    // rows: rows (plain) or columns (transposed) there are from the tile's first on;
+    // list: where set, the stored rows of a plain operand.
+    __device__ __forceinline__ void init(uint32_t wave, uint32_t lane, uint64_t ld, uint32_t rows,
+                                         const uint32_t* list) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const uint32_t u = (j * WAVES + wave) * 64 + lane;
             if constexpr (TR) {
                 const uint32_t k = u / (ROWS / 8), c = u % (ROWS / 8);
                 const uint32_t sw = (k & 3) + 4 * ((k >> 3) & 1);
-                uint32_t col = ((c / 2) ^ sw) * 16 + (c & 1) * 8;
-                col = min(col, rows - 8);
-                klane[j] = k;
-                coff[j] = col * 2;
-                voff[j] = k * (uint32_t)ld * 2 + col * 2;
+                const uint32_t col = ((c / 2) ^ sw) * 16 + (c & 1) * 8;
+                voff[j] = k * (uint32_t)ld * 2 + min(col, rows - 8) * 2;
             } else {
-                const uint32_t r = u >> 3, c = (u & 7) ^ (r & 7);
-                voff[j] = min(r, rows - 1) * (uint32_t)ld * 2 + c * 16;
+                const uint32_t c = (u & 7) ^ ((u >> 3) & 7);
+                uint32_t r = min(u >> 3, rows - 1);
+                if (list)
+                    r = list[r];
+                voff[j] = r * (uint32_t)ld * 2 + c * 16;
             }
         }
     }
 
-    // Loads the step at `p` (the operand's first element of the step's first
-    // k); left: k's there are, where fewer than a step's.
-    __device__ __forceinline__ void load(const uint16_t* p, uint64_t ld, uint32_t left,
-                                         uint32_t lds, uint32_t wave) const {
+    // Load j of the wave's kLoads of the step whose first k `srd` points to; left: k's
+    // there are from it on (past the last one, a transposed operand's last is taken).
+    __device__ __forceinline__ void load(i4v srd, int j, uint64_t ld, uint32_t left, uint32_t lds,
+                                         uint32_t wave) const {
+        uint32_t v = voff[j];
+        if constexpr (TR)
+            if (left < kMmK) {
+                const uint32_t k = ((j * WAVES + wave) * 64 + (threadIdx.x & 63)) / (ROWS / 8);
+                v -= (k - min(k, left - 1)) * (uint32_t)ld * 2;
+            }
+        dma16(srd, v, lds + (j * WAVES + wave) * 1024);
+    }
+
+    __device__ __forceinline__ void load_all(const uint16_t* p, uint64_t ld, uint32_t left,
+                                             uint32_t lds, uint32_t wave) const {
         const i4v srd = buffer_of(p);
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            uint32_t v = voff[j];
-            if constexpr (TR)
-                if (left < kMmK)
-                    v = min(klane[j], left - 1) * (uint32_t)ld * 2 + coff[j];
-            dma16(srd, v, lds + (j * WAVES + wave) * 1024);
-        }
+        for (int j = 0; j < kLoads; ++j)
+            load(srd, j, ld, left, lds, wave);
     }
 
     // Clears the k's from `left` on of a loaded transposed step.
@@ -136,15 +140,13 @@ struct MmTile {
 // A wave's fragments of COUNT groups of 16 rows.
 template <int ROWS, bool TR, int COUNT>
 struct MmFrags {
-    uint32_t at[TR ? COUNT : 2];
+    uint32_t at[TR ? 1 : 2];
 
     __device__ __forceinline__ void init(uint32_t row0, uint32_t lane) {
         if constexpr (TR) {
             const uint32_t kq = (lane >> 4) * 8 + ((lane & 15) >> 2);
             const uint32_t sw = (kq & 3) + 4 * ((kq >> 3) & 1);
-#pragma unroll
-            for (int i = 0; i < COUNT; ++i)
-                at[i] = kq * (ROWS * 2) + (((row0 / 16 + i) ^ sw) * 32) + (lane & 3) * 8;
+            at[0] = kq * (ROWS * 2) + (((row0 / 16) ^ sw) * 32) + (lane & 3) * 8;
         } else {
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
@@ -152,45 +154,77 @@ struct MmFrags {
         }
     }
 
+    // A transposed group i lies at the first one's address with bits 5 and up of i
+    // flipped: COUNT divides the 8 pairs that the chunks' order permutes, and a
+    // stage starts on a multiple of 256 bytes.
     __device__ __forceinline__ h8 read(uint32_t lds, int i, int kk) const {
+        static_assert(COUNT == 8 || COUNT == 4 || COUNT == 2 || COUNT == 1, "a power of two");
         if constexpr (TR) {
-            const uint32_t p = lds + at[i] + kk * 32 * ROWS * 2;
-            const h4 x = lds_read_tr(p), y = lds_read_tr(p + 4 * ROWS * 2);
+            typedef __attribute__((address_space(3))) h4 lds_h4;
+            lds_h4* p = (lds_h4*)(uintptr_t)((lds + at[0]) ^ (i * 32));
+            const h4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + kk * 8 * ROWS);
+            const h4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + kk * 8 * ROWS + ROWS);
             return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
             typedef __attribute__((address_space(3))) h8 lds_h8;
-            return *(const lds_h8*)(uintptr_t)(lds + at[kk] + i * 2048);
+            return ((const lds_h8*)(uintptr_t)(lds + at[kk]))[i * 128];
         }
     }
 };
 
-// Tile t of tm x tn in an order that keeps neighbours together: 8 tiles down,
-// then the next column.
+// Tile t of tm x tn in an order that keeps neighbours together: 4 tiles down,
+// then the next column (the 32 tiles that an XCD works on then share 4 row and 8
+// column panels in its L2; 8 x 4 measured 1 to 2 % slower, 16 x 2 3 %).
 __device__ __forceinline__ void mm_tile_of(uint32_t t, uint32_t tm, uint32_t tn, uint32_t* m,
                                            uint32_t* n) {
-    constexpr uint32_t G = 8;
+    constexpr uint32_t G = 4;
     const uint32_t g = t / (G * tn), r = t - g * G * tn;
     const uint32_t h = min(G, tm - g * G);
     *n = r / h;
     *m = g * G + r - *n * h;
 }
 
-// A workgroup's tile of BM x BN, shared out to WM x WN waves; STAGES steps of the
-// operands in LDS.
-template <int T_, int BM_, int BN_, int WM_, int WN_, int STAGES_, bool TA_, bool TB_>
+// A workgroup's tile of BM x BN, shared out to WM x WN waves; DEPTH steps of loads
+// under way.
+template <int T_, int BM_, int BN_, int WM_, int WN_, int DEPTH_, bool TA_, bool TB_>
 struct MmShape {
-    static constexpr int T = T_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+    static constexpr int T = T_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, DEPTH = DEPTH_;
     static constexpr bool TA = TA_, TB = TB_;
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
-    static constexpr uint32_t kStage = (BM + BN) * kMmK * 2;
+    static constexpr uint32_t kLds = (DEPTH * BM + (DEPTH + 1) * BN) * kMmK * 2;
+    // What mm_rows takes of it: of each wave kGroup rows of fragments at a time.
+    static constexpr int kGroup = MI < 4 ? MI : 4;
+    static constexpr uint32_t kRowsLds = kGroup * 16 * NI * 64 * kWaves;
+    static_assert(kRowsLds <= kLds, "fits");
 };
 
+template <int V>
+struct MmInt {
+    static constexpr int value = V;
+};
+
+// The kernel.  LDS holds DEPTH stages of a's steps and DEPTH + 1 of b's.  A step is
+// two phases of 32 k's; in each, a wave multiplies one set of fragments while it
+// reads the other set from LDS and issues loads, all between its matrix
+// instructions, a few for every row of fragments:
+//   phase 0 of step s   multiplies its first half, reads its second, loads step
+//                       s + DEPTH of b (into the stage that step s - 1 has left)
+//   (the one barrier of a step: step s + 1 has arrived for all waves, and all have
+//   read what they need of step s)
+//   phase 1             multiplies the second half, reads the first half of step
+//                       s + 1, loads step s + DEPTH of a (into step s's stage)
+// so that the matrix units wait neither for LDS nor for the loads' issue (all loads
+// of a step behind its barrier, and all reads before its products, took 3.45 and 3.56
+// ms for 16384 x 32000 x 4096 in bf16; this order takes 3.20, 1340 TFLOP/s).
 template <class S, class Epi>
 __global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi::Args e) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[S::STAGES * S::kStage];
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[S::kLds];
     using TileA = MmTile<S::BM, S::TA, S::kWaves>;
     using TileB = MmTile<S::BN, S::TB, S::kWaves>;
+    constexpr uint32_t kA = TileA::kBytes, kB = TileB::kBytes;
+    constexpr int kLoadsA = TileA::kLoads, kLoadsB = TileB::kLoads;
+    constexpr uint32_t D = S::DEPTH;
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -199,6 +233,7 @@ __global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi:
         M = min(M, *a.dyn_m);
     if (a.dyn_k)
         K = min(K, *a.dyn_k);
+    // Workgroup b runs on XCD b % 8: each XCD takes an eighth of the tiles in a row.
     const uint32_t tm = (M + S::BM - 1) / S::BM, tn = (a.N + S::BN - 1) / S::BN;
     const uint32_t total = tm * tn, per = (total + 7) / 8;
     const uint32_t t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
@@ -213,14 +248,18 @@ __global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi:
     const uint32_t per_split = (steps_all + gridDim.y - 1) / gridDim.y;
     const uint32_t s0 = min(blockIdx.y * per_split, steps_all);
     const uint32_t steps = min(per_split, steps_all - s0);
+    const uint32_t count = K - s0 * kMmK;  // k's from the split's first on
 
     TileA la;
     TileB lb;
-    la.init(wave, lane, a.a.ld, S::TA ? a.a_cols - m0 : M - m0);
-    lb.init(wave, lane, a.b.ld, S::TB ? a.b_cols - n0 : a.N - n0);
+    const bool listed = !S::TA && a.a_rows;
+    la.init(wave, lane, a.a.ld, S::TA ? a.a_cols - m0 : M - m0, listed ? a.a_rows + m0 : nullptr);
+    lb.init(wave, lane, a.b.ld, S::TB ? a.b_cols - n0 : a.N - n0, nullptr);
     const uint64_t step_a = S::TA ? kMmK * a.a.ld : kMmK, step_b = S::TB ? kMmK * a.b.ld : kMmK;
-    const uint16_t* pa = a.a.p + (S::TA ? (uint64_t)m0 : m0 * a.a.ld) + s0 * step_a;
+    const uint16_t* pa =
+        a.a.p + (S::TA ? (uint64_t)m0 : listed ? 0 : m0 * a.a.ld) + s0 * step_a;
     const uint16_t* pb = a.b.p + (S::TB ? (uint64_t)n0 : n0 * a.b.ld) + s0 * step_b;
+    const typename Epi::Row row = Epi::row(e, M, m0, tid);
 
     const uint32_t wm = wave / S::WN, wn = wave % S::WN;
     MmFrags<S::BM, S::TA, S::MI> fa;
@@ -235,123 +274,242 @@ __global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi:
         for (int j = 0; j < S::NI; ++j)
             acc[i][j] = f4{0, 0, 0, 0};
 
-    const uint32_t base = lds_offset(lds);
-    uint32_t left = K - s0 * kMmK;  // k's from the next step to load on
-    auto load = [&](uint32_t buf) {
-        la.load(pa, a.a.ld, left, base + buf * S::kStage, wave);
-        lb.load(pb, a.b.ld, left, base + buf * S::kStage + TileA::kBytes, wave);
-        pa += step_a;
-        pb += step_b;
-        left -= kMmK;
-    };
-    constexpr uint32_t kAhead = S::STAGES - 1;
+    const uint32_t base_a = lds_offset(lds), base_b = base_a + D * kA;
+    h8 x[2][S::MI], y[2][S::NI];
+    auto phase = [&](auto set, uint32_t sa, uint32_t sb, auto half, auto&& issue) {
+        constexpr int cur = decltype(set)::value, kk = decltype(half)::value;
 #pragma unroll
-    for (uint32_t s = 0; s < kAhead; ++s)
-        if (s < steps)
-            load(s);
-    uint32_t buf = 0;
-    for (uint32_t s = 0; s < steps; ++s) {
-        // Step s has arrived for this wave, then for all; the reads of step s - 1
-        // are over, so its buffer can be loaded.
-        if (s + kAhead <= steps)
-            wait_vm<(S::STAGES - 2) * (TileA::kLoads + TileB::kLoads)>();
-        else
-            wait_vm<0>();
-        wait_lds();
-        __builtin_amdgcn_s_barrier();
-        if (s + kAhead < steps)
-            load(buf == 0 ? kAhead : buf - 1);
-        const uint32_t here = K - (s0 + s) * kMmK;
-        if ((S::TA || S::TB) && here < kMmK) {
-            if constexpr (S::TA)
-                TileA::clear_tail(lds + buf * S::kStage, here, tid);
-            if constexpr (S::TB)
-                TileB::clear_tail(lds + buf * S::kStage + TileA::kBytes, here, tid);
-            __syncthreads();
-        }
-        const uint32_t sa = base + buf * S::kStage, sb = sa + TileA::kBytes;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            h8 x[S::MI], y[S::NI];
+        for (int i = 0; i < S::MI; ++i) {
+            x[1 - cur][i] = fa.read(sa, i, kk);
 #pragma unroll
             for (int j = 0; j < S::NI; ++j)
-                y[j] = fb.read(sb, j, kk);
+                if (j * S::MI / S::NI == i)
+                    y[1 - cur][j] = fb.read(sb, j, kk);
+            issue(i);
 #pragma unroll
-            for (int i = 0; i < S::MI; ++i)
-                x[i] = fa.read(sa, i, kk);
-#pragma unroll
-            for (int i = 0; i < S::MI; ++i)
-#pragma unroll
-                for (int j = 0; j < S::NI; ++j)
-                    acc[i][j] = mfma<S::T>(y[j], x[i], acc[i][j]);
+            for (int j = 0; j < S::NI; ++j)
+                acc[i][j] = mfma<S::T>(y[cur][j], x[cur][i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        buf = buf + 1 == S::STAGES ? 0 : buf + 1;
+    };
+    // Clears what a loaded step s of transposed operands has past the last k.
+    auto clear = [&](uint32_t s, uint32_t oa, uint32_t ob) {
+        const uint32_t here = count - s * kMmK;
+        if ((S::TA || S::TB) && s < steps && here < kMmK) {
+            if constexpr (S::TA)
+                TileA::clear_tail(lds + oa, here, tid);
+            if constexpr (S::TB)
+                TileB::clear_tail(lds + D * kA + ob, here, tid);
+            __syncthreads();
+        }
+    };
+    if (steps) {
+#pragma unroll
+        for (uint32_t s = 0; s < D; ++s)
+            if (s < steps) {
+                la.load_all(pa, a.a.ld, count - s * kMmK, base_a + s * kA, wave);
+                lb.load_all(pb, a.b.ld, count - s * kMmK, base_b + s * kB, wave);
+                pa += step_a;
+                pb += step_b;
+            }
+        if (steps >= D)
+            wait_vm<(D - 1) * (kLoadsA + kLoadsB)>();
+        else
+            wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        clear(0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < S::MI; ++i)
+            x[0][i] = fa.read(base_a, i, 0);
+#pragma unroll
+        for (int j = 0; j < S::NI; ++j)
+            y[0][j] = fb.read(base_b, j, 0);
+    }
+    uint32_t oa = 0, ob = 0, ob_new = D * kB;  // stages of step s, and of step s + D of b
+    for (uint32_t s = 0; s < steps; ++s) {
+        const bool more = s + D < steps;
+        const uint32_t left = count - (s + D) * kMmK;
+        const uint32_t oa1 = oa == (D - 1) * kA ? 0 : oa + kA, ob1 = ob == D * kB ? 0 : ob + kB;
+        const i4v srd_a = buffer_of(pa), srd_b = buffer_of(pb);
+        __builtin_amdgcn_sched_barrier(0);
+        phase(MmInt<0>(), base_a + oa, base_b + ob, MmInt<1>(), [&](int i) {
+            if (more)
+#pragma unroll
+                for (int j = 0; j < kLoadsB; ++j)
+                    if (j * S::MI / kLoadsB == i)
+                        lb.load(srd_b, j, a.b.ld, left, base_b + ob_new, wave);
+        });
+        // Past step s + 1's loads, those of steps s + 2 to s + D - 1 and the ones just
+        // issued may be under way.
+        wait_lds();
+        if (more)
+            wait_vm<(D - 2) * (kLoadsA + kLoadsB) + kLoadsB>();
+        else
+            wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        clear(s + 1, oa1, ob1);
+        __builtin_amdgcn_sched_barrier(0);
+        phase(MmInt<1>(), base_a + oa1, base_b + ob1, MmInt<0>(), [&](int i) {
+            if (more)
+#pragma unroll
+                for (int j = 0; j < kLoadsA; ++j)
+                    if (j * S::MI / (2 * kLoadsA) == i)
+                        la.load(srd_a, j, a.a.ld, left, base_a + oa, wave);
+        });
+        pa += step_a;
+        pb += step_b;
+        oa = oa1;
+        ob_new = ob;
+        ob = ob1;
     }
     wait_lds();
     __builtin_amdgcn_s_barrier();
-    // acc[i][j][r] is C at m = mw + 16 i + (lane & 15), n = nw + 16 j + 4 (lane >> 4) + r.
-    Epi::template finish<S>(e, acc, M, a.N, m0, n0, wm, wn, lane, lds);
+    // acc[i][j][r] is C at m = m0 + wm BM / WM + 16 i + (lane & 15),
+    // n = n0 + wn BN / WN + 16 j + 4 (lane >> 4) + r.
+    Epi::template finish<S>(e, row, acc, M, a.N, m0, n0, wm, wn, lane, lds);
 }
 
+// Hands each f4 of a wave's sums to put(m in the tile, n in the tile, f4, what
+// fetch(m, n) gave), through LDS: 16 lanes then hold 64 neighbours of one row, so that
+// whole lines are stored, and the code stands 4 times instead of 32 (it runs once and
+// comes from memory).  Four at a time, so that their fetches are under way together.
+// Four rows of fragments in a part of LDS of the wave's own, chunk c of 16 bytes of a row
+// at c ^ (row & 15) (or a smaller mask), which meets no bank twice.
+template <class S, class G, class F>
+__device__ __forceinline__ void mm_rows(f4 (&acc)[S::MI][S::NI], uint32_t wm, uint32_t wn,
+                                        uint32_t lane, unsigned char* lds, G&& fetch, F&& put) {
+    constexpr int kGroup = S::kGroup;
+    constexpr uint32_t kChunks = S::NI * 4;           // of 16 bytes in a row
+    constexpr uint32_t kAll = kGroup * 16 * kChunks;  // of a wave
+    constexpr int kBatch = kAll / 64 < 4 ? kAll / 64 : 4;
+    static_assert(kAll % (64 * kBatch) == 0, "whole batches");
+    unsigned char* mine = lds + (wm * S::WN + wn) * kAll * 16;
+    const uint32_t r = lane & 15, q = lane >> 4;
+    const uint32_t mw = wm * (S::BM / S::WM), nw = wn * (S::BN / S::WN);
+#pragma unroll
+    for (int g = 0; g < S::MI / kGroup; ++g) {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+            for (int j = 0; j < S::NI; ++j)
+                *(f4*)(mine + ((i * 16 + r) * kChunks + ((j * 4 + q) ^ (r & (kChunks - 1)))) * 16) =
+                    acc[g * kGroup + i][j];
+        wait_lds();
+#pragma unroll 1
+        for (uint32_t c0 = lane; c0 < kAll; c0 += 64 * kBatch) {
+            f4 v[kBatch], old[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t row = (c0 + k * 64) / kChunks, chunk = (c0 + k * 64) % kChunks;
+                v[k] = *(const f4*)(mine + (row * kChunks + (chunk ^ (row & (kChunks - 1)))) * 16);
+                old[k] = fetch(mw + g * kGroup * 16 + row, nw + chunk * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t row = (c0 + k * 64) / kChunks, chunk = (c0 + k * 64) % kChunks;
+                put(mw + g * kGroup * 16 + row, nw + chunk * 4, v[k], old[k]);
+            }
+        }
+        wait_lds();
+    }
+}
+
+// An epilogue has Args; Row, what a thread loads for row m0 + tid before the sums
+// (where it needs something); and finish.
+struct MmNoRow {};
 
 // What becomes of a sum: C[m, n .. n + 3], of which the first `count` exist.
 struct MmOut {
     const float* acc_in;    // sums of earlier pieces to add, or NULL
     float* acc_out;         // where to keep the sum for later pieces, or NULL
     uint64_t ldacc;         // a multiple of 4
-    void* out;              // else: times scale (and *factor) into out's row list[m]
-    uint64_t ldo;
+    void* out;              // else: times scale (and *factor) into out's row list[m],
+    uint64_t ldo;           // added to what is there where `add` is set
     const uint32_t* list;
     const float* factor;
     float scale;
     int type, add;
 
-    __device__ __forceinline__ void put(uint32_t m, uint32_t n, uint32_t count, f4 v) const {
+    __device__ __forceinline__ uint64_t at(uint32_t m, uint32_t n) const {
+        return (list ? list[m] : m) * ldo + n;
+    }
+
+    // What put needs of memory: the earlier pieces' sums, or what out holds.  (Both never
+    // occur together: dx has pieces, dw is added to.)
+    __device__ __forceinline__ f4 fetch(uint32_t m, uint32_t n, uint32_t count) const {
         if (acc_in)
-            v += *(const f4*)(acc_in + m * ldacc + n);
+            return *(const f4*)(acc_in + m * ldacc + n);
+        f4 v = {0, 0, 0, 0};
+        if (!add)
+            return v;
+        const uint64_t e = at(m, n);
+        if (type == kF32) {
+            typedef f4 any __attribute__((aligned(4)));
+            const float* p = (const float*)out + e;
+            if (count >= 4)
+                return *(const any*)p;
+#pragma unroll
+            for (uint32_t r = 0; r < 3; ++r)
+                if (r < count)
+                    v[r] = p[r];
+        } else {
+            typedef u2 any __attribute__((aligned(2)));
+            const uint16_t* p = (const uint16_t*)out + e;
+            u2 o = {0, 0};
+            if (count >= 4) {
+                o = *(const any*)p;
+            } else {
+                o.x = p[0];
+                if (count > 1)
+                    o.x |= (uint32_t)p[1] << 16;
+                if (count > 2)
+                    o.y = p[2];
+            }
+            v = type == kBF16 ? f4{bf16lo(o.x), bf16hi(o.x), bf16lo(o.y), bf16hi(o.y)}
+                              : f4{f16lo(o.x), f16hi(o.x), f16lo(o.y), f16hi(o.y)};
+        }
+        return v;
+    }
+
+    __device__ __forceinline__ void put(uint32_t m, uint32_t n, uint32_t count, f4 v,
+                                        f4 old) const {
+        if (acc_in)
+            v += old;
         if (acc_out) {
             *(f4*)(acc_out + m * ldacc + n) = v;
             return;
         }
-        const float f = factor ? scale * *factor : scale;
-        v *= f;
-        const uint64_t e = (list ? list[m] : m) * ldo + n;
+        v *= factor ? scale * *factor : scale;
+        if (add)
+            v += old;
+        const uint64_t e = at(m, n);
         if (type == kF32) {
-            typedef f4 at __attribute__((aligned(4)));
+            typedef f4 any __attribute__((aligned(4)));
             float* p = (float*)out + e;
             if (count >= 4) {
-                if (add)
-                    v += *(const at*)p;
-                *(at*)p = v;
-            } else {
-                for (uint32_t r = 0; r < 3; ++r)
-                    if (r < count)
-                        p[r] = add ? p[r] + v[r] : v[r];
+                *(any*)p = v;
+                return;
             }
+#pragma unroll
+            for (uint32_t r = 0; r < 3; ++r)
+                if (r < count)
+                    p[r] = v[r];
         } else {
-            typedef u2 at __attribute__((aligned(2)));
+            typedef u2 any __attribute__((aligned(2)));
             uint16_t* p = (uint16_t*)out + e;
+            const u2 o = type == kBF16
+                             ? u2{pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3])}
+                             : u2{pack_f16_rne(apart(v[0]), apart(v[1])),
+                                  pack_f16_rne(apart(v[2]), apart(v[3]))};
             if (count >= 4) {
-                if (add) {
-                    const u2 o = *(const at*)p;
-                    if (type == kBF16)
-                        v += f4{bf16lo(o.x), bf16hi(o.x), bf16lo(o.y), bf16hi(o.y)};
-                    else
-                        v += f4{f16lo(o.x), f16hi(o.x), f16lo(o.y), f16hi(o.y)};
-                }
-                *(at*)p = type == kBF16 ? u2{pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3])}
-                                        : u2{pack_f16_rne(apart(v[0]), apart(v[1])),
-                                             pack_f16_rne(apart(v[2]), apart(v[3]))};
-            } else {
-                for (uint32_t r = 0; r < 3; ++r)
-                    if (r < count) {
-                        float x = v[r];
-                        if (add)
-                            x += type == kBF16 ? bf16lo(p[r]) : f16lo(p[r]);
-                        p[r] = (uint16_t)(type == kBF16 ? pack_bf16_rne(x, x)
-                                                        : pack_f16_rne(apart(x), apart(x)));
-                    }
+                *(any*)p = o;
+                return;
             }
+            p[0] = (uint16_t)o.x;
+            if (count > 1)
+                p[1] = (uint16_t)(o.x >> 16);
+            if (count > 2)
+                p[2] = (uint16_t)o.y;
         }
     }
 };
@@ -364,29 +522,31 @@ struct MmSum {
         float* part;
         uint64_t rows, ld;
     };
+    using Row = MmNoRow;
+    static __device__ __forceinline__ Row row(const Args&, uint32_t, uint32_t, uint32_t) {
+        return {};
+    }
     template <class S>
-    static __device__ __forceinline__ void finish(const Args& e, f4 (&acc)[S::MI][S::NI],
-                                                  uint32_t M, uint32_t N, uint32_t m0, uint32_t n0,
-                                                  uint32_t wm, uint32_t wn, uint32_t lane,
-                                                  unsigned char*) {
-        const uint32_t mw = m0 + wm * (S::BM / S::WM) + (lane & 15);
-        const uint32_t nw = n0 + wn * (S::BN / S::WN) + (lane >> 4) * 4;
-#pragma unroll
-        for (int i = 0; i < S::MI; ++i) {
-            const uint32_t m = mw + i * 16;
-            if (m >= M)
-                continue;
-#pragma unroll
-            for (int j = 0; j < S::NI; ++j) {
-                const uint32_t n = nw + j * 16;
-                if (n >= N)
-                    continue;
-                if (e.part)
-                    *(f4*)(e.part + (blockIdx.y * e.rows + m) * e.ld + n) = acc[i][j];
+    static __device__ __forceinline__ void finish(const Args& e, const Row&,
+                                                  f4 (&acc)[S::MI][S::NI], uint32_t M, uint32_t N,
+                                                  uint32_t m0, uint32_t n0, uint32_t wm,
+                                                  uint32_t wn, uint32_t lane, unsigned char* lds) {
+        const bool part = e.part != nullptr;
+        mm_rows<S>(
+            acc, wm, wn, lane, lds,
+            [&](uint32_t r, uint32_t c) {
+                const uint32_t m = m0 + r, n = n0 + c;
+                return !part && m < M && n < N ? e.o.fetch(m, n, N - n) : f4{0, 0, 0, 0};
+            },
+            [&](uint32_t r, uint32_t c, f4 v, f4 old) {
+                const uint32_t m = m0 + r, n = n0 + c;
+                if (m >= M || n >= N)
+                    return;
+                if (part)
+                    *(f4*)(e.part + (blockIdx.y * e.rows + m) * e.ld + n) = v;
                 else
-                    e.o.put(m, n, N - n, acc[i][j]);
-            }
-        }
+                    e.o.put(m, n, N - n, v, old);
+            });
     }
 };
 
@@ -400,10 +560,11 @@ __global__ __launch_bounds__(256) static void mm_join_kernel(MmSum::Args e, uint
     const uint64_t total = (uint64_t)M * groups;
     for (uint64_t g = blockIdx.x * 256ull + threadIdx.x; g < total; g += gridDim.x * 256ull) {
         const uint32_t m = (uint32_t)(g / groups), n = (uint32_t)(g - (uint64_t)m * groups) * 4;
+        const f4 old = e.o.fetch(m, n, N - n);
         f4 v = *(const f4*)(e.part + m * e.ld + n);
         for (uint32_t s = 1; s < splits; ++s)
             v += *(const f4*)(e.part + (s * e.rows + m) * e.ld + n);
-        e.o.put(m, n, N - n, v);
+        e.o.put(m, n, N - n, v, old);
     }
 }
 

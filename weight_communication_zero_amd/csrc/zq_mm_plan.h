@@ -8,8 +8,8 @@
 
 namespace zq {
 
-// The tiles there are: 256 x 256 by 8 waves (128 KiB of LDS, one workgroup a
-// CU), 128 x 128 by 4 waves (64 KiB, two a CU).
+// The tiles there are: 256 x 256 by 8 waves (160 KiB of LDS, one workgroup a
+// CU), 128 x 128 by 4 waves (80 KiB, two a CU).
 enum MmTileKind : int { kTile256 = 0, kTile128 = 1 };
 
 struct MmPlan {
