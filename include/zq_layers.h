@@ -105,7 +105,7 @@ size_t zq_linear_grad_workspace(size_t n_tok, uint64_t out_dim, uint64_t in_dim)
  *   lse[t]  = log of the sum over v of exp(z[t, v])
  *   loss[t] = lse[t] - z[t, ids[t]]
  * A token whose id is outside [0, rows) is left out: its loss and lse are +0 and
- * its x is not read (padding may hold anything).
+ * its x has no effect (padding may hold anything).
  *
  *   x      [n_tok, dim] bf16 or fp16 (dtype), read only.
  *   w      [rows, dim] of dtype, read only.

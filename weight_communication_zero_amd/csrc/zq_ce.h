@@ -13,7 +13,8 @@ struct CeScalars {
     float up, down;    // the power of two that scales q, and its inverse
 };
 
-// The tokens that count, in order: r-th of them is token list[r].
+// The tokens that count, in order: the r-th of them is token list[r].  Behind them
+// stand the tokens that are left out, the last one first.
 struct CeTokens {
     CeScalars* scalars;
     uint32_t* list;
@@ -31,14 +32,24 @@ struct CePrepArgs {
 
 // Gathers the tokens that count.  One workgroup: 2^14 tokens take two rounds (of
 // 8192 ids, 8 a thread, in flight together), and positions need no second pass.
-static __global__ __launch_bounds__(1024) void ce_prep_kernel(CePrepArgs a) {
+template <bool GRAD>
+__global__ __launch_bounds__(1024) void ce_prep_kernel(CePrepArgs a) {
     __shared__ uint32_t sums[16], maxima[16];
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t count = 0, top = 0;
     for (uint32_t base = 0; base < a.n_tok; base += 8192) {
         const uint32_t first = base + wave * 512 + lane;
+        const uint32_t last = a.n_tok - 1;
         uint64_t id[8];
-        load_ids<8>(a.ids, a.id64, [&](int j) { return min(first + j * 64, a.n_tok - 1); }, id);
+        load_ids<8>(a.ids, a.id64, [&](int j) { return min(first + j * 64, last); }, id);
+        float lse[8], g[8];
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                lse[j] = a.lse[min(first + j * 64, last)];
+                g[j] = a.dloss[min(first + j * 64, last)];
+            }
+        }
         uint64_t there[8];
         uint32_t mine = 0;
 #pragma unroll
@@ -65,32 +76,40 @@ static __global__ __launch_bounds__(1024) void ce_prep_kernel(CePrepArgs a) {
             if (there[j] >> lane & 1) {
                 a.t.list[r] = t;
                 a.t.target[r] = (uint32_t)id[j];
-                if (a.dloss) {
-                    const float g = a.dloss[t];
-                    a.t.lse[r] = a.lse[t];
-                    a.t.dloss[r] = g;
-                    top = max(top, absbits(g) < 0x7F800000u ? absbits(g) : 0);
+                if constexpr (GRAD) {
+                    a.t.lse[r] = lse[j];
+                    a.t.dloss[r] = g[j];
+                    top = max(top, absbits(g[j]) < 0x7F800000u ? absbits(g[j]) : 0);
                 }
-            } else if (a.loss && t < a.n_tok) {
-                a.loss[t] = 0.0f;
-                a.lse_out[t] = 0.0f;
+            } else if (t < a.n_tok) {
+                // t - r tokens before this one are left out.
+                a.t.list[last - (t - r)] = t;
+                if constexpr (!GRAD) {
+                    a.loss[t] = 0.0f;
+                    a.lse_out[t] = 0.0f;
+                }
             }
         }
     }
-    top = group_max<64>(top);
-    if (lane == 0)
-        maxima[wave] = top;
-    __syncthreads();
+    if constexpr (GRAD) {
+        top = group_max<64>(top);
+        if (lane == 0)
+            maxima[wave] = top;
+        __syncthreads();
+    }
     if (threadIdx.x == 0) {
-        for (int w = 0; w < 16; ++w)
-            top = max(top, maxima[w]);
-        // 2^(14 - exponent): exponents of a power of two and of its inverse stay normal.
-        int shift = 0;
-        if (a.scaled && top)
-            shift = min(max(141 - (int)(top >> 23), -120), 120);
         a.t.scalars->count = count;
-        a.t.scalars->up = bitsf((uint32_t)(127 + shift) << 23);
-        a.t.scalars->down = bitsf((uint32_t)(127 - shift) << 23);
+        if constexpr (GRAD) {
+            for (int w = 0; w < 16; ++w)
+                top = max(top, maxima[w]);
+            // 2^(14 - exponent): exponents of a power of two and of its inverse stay
+            // normal.
+            int shift = 0;
+            if (a.scaled && top)
+                shift = min(max(141 - (int)(top >> 23), -120), 120);
+            a.t.scalars->up = bitsf((uint32_t)(127 + shift) << 23);
+            a.t.scalars->down = bitsf((uint32_t)(127 - shift) << 23);
+        }
     }
 }
 
@@ -143,13 +162,15 @@ inline CeTokens ce_tokens(const CeLayout& l, char* ws) {
             (float*)(ws + l.lse), (float*)(ws + l.dloss)};
 }
 
-inline hipError_t ce_prep(const CeArgs& a, const CeTokens& t, bool scaled, hipStream_t stream) {
+template <bool GRAD>
+hipError_t ce_prep(const CeArgs& a, const CeTokens& t, bool scaled, hipStream_t stream) {
     CePrepArgs p = {a.ids, a.id64, a.n_tok, a.rows, scaled, a.lse, a.dloss, a.loss, a.lse_out, t};
     void* args[] = {&p};
-    return hipLaunchKernel((const void*)&ce_prep_kernel, dim3(1), dim3(1024), args, 0, stream);
+    return hipLaunchKernel((const void*)&ce_prep_kernel<GRAD>, dim3(1), dim3(1024), args, 0,
+                           stream);
 }
 
-// The hidden states of the tokens that count.
+// The hidden states of the tokens that count, and zeros for dx where one is left out.
 template <int T>
 hipError_t ce_stage_x(const CeArgs& a, const CeLayout& l, const CeTokens& t, char* ws,
                       hipStream_t stream) {
@@ -161,6 +182,7 @@ hipError_t ce_stage_x(const CeArgs& a, const CeLayout& l, const CeTokens& t, cha
     s.out = (uint16_t*)(ws + l.x);
     s.list = t.list;
     s.count = &t.scalars->count;
+    s.clear = (uint16_t*)a.dx;
     return launch_stage<T>(s, T, stream);
 }
 

@@ -64,25 +64,6 @@ struct Residual {
     }
 };
 
-struct LeftOutArgs {
-    const void* ids;
-    uint32_t id64, n_tok, rows, dim;
-    uint16_t* dx;
-};
-
-// Clears the rows of dx whose tokens are left out: a wave a token.
-__global__ __launch_bounds__(256) void left_out_kernel(LeftOutArgs a) {
-    for (uint32_t t = (uint32_t)wave_id(); t < a.n_tok; t += (uint32_t)wave_count()) {
-        uint64_t id[1];
-        load_ids<1>(a.ids, a.id64, [&](int) { return t; }, id);
-        if (id[0] < a.rows)
-            continue;
-        uint16_t* row = a.dx + (uint64_t)t * a.dim;
-        for (uint32_t j = (uint32_t)lane_id(); j < a.dim; j += kWave)
-            row[j] = 0;
-    }
-}
-
 CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
     CeLayout l = {};
     l.kp = round_up(dim, kMmK);
@@ -113,16 +94,9 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
     const CeLayout l = layout(a.n_tok, a.rows, a.dim, a.piece);
     char* ws = (char*)a.workspace;
     const CeTokens tok = ce_tokens(l, ws);
-    hipError_t st = ce_prep(a, tok, T == kF16, stream);
+    hipError_t st = ce_prep<true>(a, tok, T == kF16, stream);
     if (st == hipSuccess)
         st = ce_stage_x<T>(a, l, tok, ws, stream);
-    if (st == hipSuccess && a.dx) {
-        LeftOutArgs o = {a.ids, a.id64, a.n_tok, a.rows, a.dim, (uint16_t*)a.dx};
-        void* args[] = {&o};
-        st = hipLaunchKernel((const void*)&left_out_kernel,
-                             dim3(std::min<uint32_t>((a.n_tok + 3) / 4, 4096)), dim3(256), args, 0,
-                             stream);
-    }
     const MmOperand x = {(const uint16_t*)(ws + l.x), l.kp};
     const MmOperand q = {(const uint16_t*)(ws + l.q), l.piece};
     float* acc = (float*)(ws + l.acc);

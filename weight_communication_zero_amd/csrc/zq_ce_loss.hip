@@ -28,28 +28,43 @@ struct Stats {
         float scale;
         f2* part;          // [tile of the piece][ld]
         uint64_t ld;
-        const uint32_t* target;
         uint32_t v0;       // the piece's first row
         float* z_target;
+        const uint32_t* target;  // of the tokens that count, or NULL: all tokens, by
+        const void* ids;         // their ids
+        uint32_t id64;
     };
 
-    using Row = MmNoRow;
-    static __device__ __forceinline__ Row row(const Args&, uint32_t, uint32_t, uint32_t) {
-        return {};
+    // A token's target in the piece (a large number where it lies outside).
+    struct Row {
+        uint32_t target;
+    };
+    static __device__ __forceinline__ Row row(const Args& e, uint32_t M, uint32_t m0,
+                                              uint32_t tid) {
+        const uint32_t m = min(m0 + tid, M - 1);
+        if (e.target)
+            return {e.target[m] - e.v0};
+        uint64_t id[1];
+        load_ids<1>(e.ids, e.id64, [&](int) { return m; }, id);
+        return {id[0] <= 0x7FFFFFFFu ? (uint32_t)id[0] - e.v0 : 0xFFFFFFFFu};
     }
 
     template <class S>
-    static __device__ __forceinline__ void finish(const Args& e, const Row&,
+    static __device__ __forceinline__ void finish(const Args& e, const Row& mine,
                                                   f4 (&acc)[S::MI][S::NI], uint32_t M, uint32_t N,
                                                   uint32_t m0, uint32_t n0, uint32_t wm,
                                                   uint32_t wn, uint32_t lane, unsigned char* lds) {
-        f2* pair = (f2*)lds;  // [WN][BM]
+        f2* pair = (f2*)lds;                              // [WN][BM]
+        uint32_t* targets = (uint32_t*)(pair + S::WN * S::BM);  // [BM]
+        static_assert(S::kThreads >= S::BM && S::BM * (8 * S::WN + 4) <= S::kLds, "fits");
+        if (threadIdx.x < S::BM)
+            targets[threadIdx.x] = mine.target;
+        __syncthreads();
         const uint32_t nw = n0 + wn * (S::BN / S::WN) + (lane >> 4) * 4;
 #pragma unroll
         for (int i = 0; i < S::MI; ++i) {
             const uint32_t r = wm * (S::BM / S::WM) + i * 16 + (lane & 15), m = m0 + r;
-            uint32_t target = m < M ? e.target[m] - e.v0 : N;
-            target = target < N ? target : 0xFFFFFFFFu;
+            const uint32_t target = m < M && targets[r] < N ? targets[r] : 0xFFFFFFFFu;
             float top = -__builtin_inff(), z_target = 0.0f;
 #pragma unroll
             for (int j = 0; j < S::NI; ++j)
@@ -99,33 +114,54 @@ struct Stats {
 struct JoinArgs {
     const f2* part;
     uint64_t ld;
-    uint32_t tiles, first, last;
+    uint32_t tiles, first, last, n_tok, rows;
     f2* run;
     const float* z_target;
-    CeTokens t;
+    const uint32_t *list, *count;  // of the tokens that count, or NULL: all tokens, by
+    const void* ids;               // their ids
+    uint32_t id64;
     float *loss, *lse;
 };
 
-// Joins a piece's tiles with what earlier pieces gave.  16 tokens a workgroup, 16
-// threads each: thread k takes tiles k, k + 16, ...
+// Joins a piece's tiles with what earlier pieces gave.  ROWS tokens a workgroup,
+// K = 256 / ROWS threads each: thread k takes tiles k, k + K, ..., and the threads'
+// pairs are joined by halves.
+template <uint32_t ROWS>
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
-    __shared__ f2 part[16][17];
-    const uint32_t row = threadIdx.x & 15, k = threadIdx.x >> 4;
-    const uint32_t m = blockIdx.x * 16 + row, count = a.t.scalars->count;
+    constexpr uint32_t K = 256 / ROWS;
+    __shared__ f2 part[K][ROWS];
+    const uint32_t row = threadIdx.x % ROWS, k = threadIdx.x / ROWS;
+    const uint32_t m = blockIdx.x * ROWS + row;
+    const uint32_t count = a.count ? *a.count : a.n_tok;
     f2 mine = {-__builtin_inff(), 0.0f};
     auto add = [&mine](f2 p) {
         const float top = __builtin_fmaxf(mine.x, p.x), ref = reference(top);
         mine = f2{top, rebased(mine, ref) + rebased(p, ref)};
     };
-    if (m < count)
-        for (uint32_t t = k; t < a.tiles; t += 16)
+    if (m < count) {
+        uint32_t t = k;
+        for (; t + 3 * K < a.tiles; t += 4 * K) {  // four loads under way
+            f2 p[4];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                p[j] = a.part[(t + j * K) * a.ld + m];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                add(p[j]);
+        }
+        for (; t < a.tiles; t += K)
             add(a.part[t * a.ld + m]);
-    part[k][row] = mine;
-    __syncthreads();
+    }
+#pragma unroll
+    for (uint32_t h = K / 2; h > 0; h /= 2) {
+        part[k][row] = mine;
+        __syncthreads();
+        if (k < h)
+            add(part[k + h][row]);
+        __syncthreads();
+    }
     if (k != 0 || m >= count)
         return;
-    for (int j = 1; j < 16; ++j)
-        add(part[j][row]);
     if (!a.first)
         add(a.run[m]);
     if (!a.last) {
@@ -133,9 +169,31 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
         return;
     }
     const float ref = reference(mine.x), log_sum = logf(mine.y);
-    const uint32_t t = a.t.list[m];
+    uint32_t t = m;
+    if (a.list) {
+        t = a.list[m];
+    } else {
+        uint64_t id[1];
+        load_ids<1>(a.ids, a.id64, [&](int) { return m; }, id);
+        if (id[0] >= a.rows) {
+            a.lse[t] = 0.0f;
+            a.loss[t] = 0.0f;
+            return;
+        }
+    }
     a.lse[t] = ref + log_sum;
     a.loss[t] = (ref - a.z_target[m]) + log_sum;
+}
+
+// Up to this many tokens the loss is formed for all of them, also those that are left
+// out: no tile's worth of work is saved by gathering, and its launch is (a token, 4096
+// x 32000: 67 us in place of 77).
+constexpr uint32_t kAllTokens = 512;
+
+// Whether the hidden states are read where they lie (else staged): rows whose width is a
+// whole number of steps, within the 4 GiB that a list's rows may span.
+bool x_in_place(uint32_t n_tok, uint32_t dim) {
+    return dim % kMmK == 0 && (n_tok <= kAllTokens || (uint64_t)n_tok * dim * 2 < (uint64_t)1 << 32);
 }
 
 CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
@@ -150,7 +208,7 @@ CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
     l.logits = mm_plan(n_tok, l.piece, l.kp, false);
     CeTake take;
     ce_take_tokens(l, take, n_tok, false);
-    l.part = take(div_up(l.piece, tile_edge(l.logits.kind)) * n_pad * 8);
+    l.part = take(div_up(l.piece, tile_cols(l.logits.kind)) * n_pad * 8);
     l.run = take(n_pad * 8);
     l.z_target = take(n_pad * 4);
     l.total = take.at;
@@ -162,8 +220,10 @@ hipError_t launch(const CeArgs& a, int w_type, hipStream_t stream) {
     const CeLayout l = layout(a.n_tok, a.rows, a.dim, a.piece);
     char* ws = (char*)a.workspace;
     const CeTokens tok = ce_tokens(l, ws);
-    hipError_t st = ce_prep(a, tok, false, stream);
-    if (st == hipSuccess)
+    const bool all = a.n_tok <= kAllTokens && x_in_place(a.n_tok, a.dim);
+    hipError_t st = all ? hipSuccess : ce_prep<false>(a, tok, false, stream);
+    const uint32_t* count = all ? nullptr : &tok.scalars->count;
+    if (st == hipSuccess && !x_in_place(a.n_tok, a.dim))
         st = ce_stage_x<T>(a, l, tok, ws, stream);
     for (uint32_t i = 0; i < l.n_pieces && st == hipSuccess; ++i) {
         const uint32_t v0 = i * l.piece, n = l.rows_of(i, a.rows);
@@ -172,20 +232,33 @@ hipError_t launch(const CeArgs& a, int w_type, hipStream_t stream) {
         if (st != hipSuccess)
             break;
         m.a = {(const uint16_t*)(ws + l.x), l.kp};
+        if (x_in_place(a.n_tok, a.dim)) {
+            m.a.p = (const uint16_t*)a.x;
+            m.a_rows = all ? nullptr : tok.list;
+        }
         m.M = a.n_tok;
         m.N = n;
         m.K = (uint32_t)l.kp;
-        m.dyn_m = &tok.scalars->count;
-        Stats::Args e = {a.scale, (f2*)(ws + l.part), round_up(a.n_tok, 256), tok.target, v0,
-                         (float*)(ws + l.z_target)};
+        m.dyn_m = count;
+        Stats::Args e = {a.scale,
+                         (f2*)(ws + l.part),
+                         round_up(a.n_tok, 256),
+                         v0,
+                         (float*)(ws + l.z_target),
+                         all ? nullptr : tok.target,
+                         a.ids,
+                         a.id64};
         st = launch_mm<T, false, false, Stats>(m, e, l.logits, stream);
         if (st != hipSuccess)
             break;
-        JoinArgs j = {e.part, e.ld, (uint32_t)div_up(n, tile_edge(l.logits.kind)), i == 0,
-                      i + 1 == l.n_pieces, (f2*)(ws + l.run), e.z_target, tok, a.loss, a.lse_out};
+        JoinArgs j = {e.part, e.ld, (uint32_t)div_up(n, tile_cols(l.logits.kind)), i == 0,
+                      i + 1 == l.n_pieces, a.n_tok, a.rows, (f2*)(ws + l.run), e.z_target,
+                      all ? nullptr : tok.list, count, a.ids, a.id64, a.loss, a.lse_out};
         void* args[] = {&j};
-        st = hipLaunchKernel((const void*)&join_kernel, dim3((a.n_tok + 15) / 16), dim3(256), args,
-                             0, stream);
+        // Few tokens: more threads each, so that no thread walks a long line of tiles.
+        const uint32_t rows = a.n_tok <= 512 ? 2 : 16;
+        st = hipLaunchKernel(rows == 2 ? (const void*)&join_kernel<2> : (const void*)&join_kernel<16>,
+                             dim3((a.n_tok + rows - 1) / rows), dim3(256), args, 0, stream);
     }
     return st;
 }

@@ -75,9 +75,17 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
 }
 
 // The LDS side of one operand of ROWS rows.  Stored by 16-byte chunks so that
-// the reads below meet no bank twice:
+// the reads below meet no bank twice (transposed tiles of fewer than 128 rows apart):
 //   plain       row r, chunk c of 8 at (r, c ^ (r & 7))
-//   transposed  k, pair of chunks q at (k, q ^ ((k & 3) + 4 (k >> 3 & 1)))
+//   transposed  k, pair of chunks q at (k, q ^ mm_turn(k))
+
+// The turn of a transposed tile's row of ROWS / 16 pairs: the 16 k's of one read are
+// 8 q + 0 .. 3 for q = 0 .. 3.
+template <int ROWS>
+__device__ __forceinline__ uint32_t mm_turn(uint32_t k) {
+    return ((k & 3) + 4 * ((k >> 3) & 1)) & (ROWS >= 128 ? 7 : ROWS / 16 - 1);
+}
+
 template <int ROWS, bool TR, int WAVES>
 struct MmTile {
     static constexpr uint32_t kBytes = ROWS * kMmK * 2;
@@ -95,8 +103,7 @@ struct MmTile {
             const uint32_t u = (j * WAVES + wave) * 64 + lane;
             if constexpr (TR) {
                 const uint32_t k = u / (ROWS / 8), c = u % (ROWS / 8);
-                const uint32_t sw = (k & 3) + 4 * ((k >> 3) & 1);
-                const uint32_t col = ((c / 2) ^ sw) * 16 + (c & 1) * 8;
+                const uint32_t col = ((c / 2) ^ mm_turn<ROWS>(k)) * 16 + (c & 1) * 8;
                 voff[j] = k * (uint32_t)ld * 2 + min(col, rows - 8) * 2;
             } else {
                 const uint32_t c = (u & 7) ^ ((u >> 3) & 7);
@@ -145,8 +152,7 @@ struct MmFrags {
     __device__ __forceinline__ void init(uint32_t row0, uint32_t lane) {
         if constexpr (TR) {
             const uint32_t kq = (lane >> 4) * 8 + ((lane & 15) >> 2);
-            const uint32_t sw = (kq & 3) + 4 * ((kq >> 3) & 1);
-            at[0] = kq * (ROWS * 2) + (((row0 / 16) ^ sw) * 32) + (lane & 3) * 8;
+            at[0] = kq * (ROWS * 2) + (((row0 / 16) ^ mm_turn<ROWS>(kq)) * 32) + (lane & 3) * 8;
         } else {
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
@@ -154,8 +160,8 @@ struct MmFrags {
         }
     }
 
-    // A transposed group i lies at the first one's address with bits 5 and up of i
-    // flipped: COUNT divides the 8 pairs that the chunks' order permutes, and a
+    // A transposed group i lies at the first one's address with the bits of 32 i
+    // flipped: row0 / 16 is a multiple of COUNT, at most 8 and a power of two, and a
     // stage starts on a multiple of 256 bytes.
     __device__ __forceinline__ h8 read(uint32_t lds, int i, int kk) const {
         static_assert(COUNT == 8 || COUNT == 4 || COUNT == 2 || COUNT == 1, "a power of two");

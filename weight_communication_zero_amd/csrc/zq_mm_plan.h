@@ -8,9 +8,10 @@
 
 namespace zq {
 
-// The tiles there are: 256 x 256 by 8 waves (160 KiB of LDS, one workgroup a
-// CU), 128 x 128 by 4 waves (80 KiB, two a CU).
-enum MmTileKind : int { kTile256 = 0, kTile128 = 1 };
+// The tiles there are: 256 x 256 by 8 waves (160 KiB of LDS, one workgroup a CU),
+// 128 x 128 by 4 waves (80 KiB, two a CU), and for few rows or columns 32 x 64 by 4
+// waves (56 KiB).
+enum MmTileKind : int { kTile256 = 0, kTile128 = 1, kTileSmall = 2 };
 
 struct MmPlan {
     int kind;
@@ -19,7 +20,12 @@ struct MmPlan {
 
 constexpr uint32_t kMaxSplits = 32;
 
-constexpr uint32_t tile_edge(int kind) { return kind == kTile256 ? 256 : 128; }
+constexpr uint32_t tile_rows(int kind) {
+    return kind == kTile256 ? 256 : kind == kTile128 ? 128 : 32;
+}
+constexpr uint32_t tile_cols(int kind) {
+    return kind == kTile256 ? 256 : kind == kTile128 ? 128 : 64;
+}
 
 inline uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 inline uint64_t round_up(uint64_t a, uint64_t b) { return div_up(a, b) * b; }
@@ -29,23 +35,25 @@ inline uint64_t part_floats(const MmPlan& p, uint64_t M, uint64_t N) {
     return p.splits > 1 ? p.splits * M * round_up(N, 4) : 0;
 }
 
-// The tile and the splits of the least time by a simple model: rounds of
-// workgroups over the CUs, each of its steps (with all CUs at work a step of 64 k's
-// takes 1.8 us for a 256-tile and 1.0 us for a 128-tile, two of which share a CU) and
-// of 3 us around them; and for a split the partial sums' way to memory and back.
+// The tile and the splits of the least time by a simple model: rounds of workgroups
+// over the CUs, each of its steps and of 4 us around them, and for a split the partial
+// sums' way to memory and back.  What a step of 64 k's takes, measured with all CUs at
+// work: 1.6 us for a 256-tile, 0.95 us for a 128-tile (two of which share a CU), 0.35 us
+// for a small one (two).  A small tile also reads its operands 4 to 8 times as often:
+// with M, N and K large it is never the least.
 inline MmPlan mm_plan(uint64_t M, uint64_t N, uint64_t K, bool may_split) {
+    constexpr double kStepUs[3] = {1.6, 0.95, 0.35};
+    constexpr uint64_t kSlots[3] = {256, 512, 512};
     const uint64_t steps = std::max<uint64_t>(div_up(K, kMmK), 1);
     MmPlan best = {kTile256, 1};
     double least = 1e30;
-    for (int kind : {kTile256, kTile128}) {
-        const uint64_t e = tile_edge(kind), tiles = div_up(M, e) * div_up(N, e);
-        const uint64_t slots = kind == kTile256 ? 256 : 512;
-        const double step_us = kind == kTile256 ? 1.8 : 1.0;
+    for (int kind : {kTile256, kTile128, kTileSmall}) {
+        const uint64_t tiles = div_up(M, tile_rows(kind)) * div_up(N, tile_cols(kind));
         for (uint64_t s = 1; s <= (may_split ? kMaxSplits : 1) && (s == 1 || steps / s >= 4); ++s) {
-            const double rounds = (double)div_up(tiles * s, slots);
-            double us = rounds * ((double)div_up(steps, s) * step_us + 3.0);
+            const double rounds = (double)div_up(tiles * s, kSlots[kind]);
+            double us = rounds * ((double)div_up(steps, s) * kStepUs[kind] + 4.0);
             if (s > 1)
-                us += 3.0 + (double)(2 * s * M * N) * 4 / 4e6;
+                us += 4.0 + (double)(2 * s * M * N) * 4 / 4e6;
             if (us < least) {
                 least = us;
                 best = {kind, (uint32_t)s};
@@ -72,7 +80,9 @@ hipError_t launch_mm(const MmArgs& a, const typename Epi::Args& e, const MmPlan&
                      hipStream_t stream) {
     if (p.kind == kTile256)
         return launch_mm_shape<MmShape<T, 256, 256, 2, 4, 2, TA, TB>, Epi>(a, e, p.splits, stream);
-    return launch_mm_shape<MmShape<T, 128, 128, 2, 2, 2, TA, TB>, Epi>(a, e, p.splits, stream);
+    if (p.kind == kTile128)
+        return launch_mm_shape<MmShape<T, 128, 128, 2, 2, 2, TA, TB>, Epi>(a, e, p.splits, stream);
+    return launch_mm_shape<MmShape<T, 32, 64, 1, 4, 4, TA, TB>, Epi>(a, e, p.splits, stream);
 }
 
 // A product into MmOut, its partial sums (where split) in `part`.

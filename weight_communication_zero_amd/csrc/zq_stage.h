@@ -17,6 +17,8 @@ struct StageArgs {
     uint16_t* out;
     const uint32_t* list;   // row r is src's row list[r], for r < *count
     const uint32_t* count;
+    uint16_t* clear;        // where set, rows list[r] of `dim` elements, r from *count on,
+                            // are cleared in it
 };
 
 // A lane per group of 8 elements of the result.
@@ -24,11 +26,17 @@ template <int T, int IN, bool WHOLE>
 __global__ __launch_bounds__(256) void stage_kernel(StageArgs a) {
     const uint32_t rows = a.count ? min(a.rows, *a.count) : a.rows;
     const uint32_t per_row = a.ld / 8;
-    const uint64_t groups = (uint64_t)rows * per_row;
+    const uint64_t groups = (uint64_t)(a.clear ? a.rows : rows) * per_row;
     for (uint64_t g = blockIdx.x * 256ull + threadIdx.x; g < groups; g += gridDim.x * 256ull) {
         const uint32_t r = (uint32_t)(g / per_row);
         const uint32_t c = (uint32_t)(g - (uint64_t)r * per_row) * 8;
         Raw<T, 8> v = {{0, 0, 0, 0}};
+        if (r >= rows) {
+            if (c < a.dim)
+                store_group<T, 8, WHOLE, false>(v, a.clear, a.list[r] * a.dim + c,
+                                                (uint32_t)(a.dim - c));
+            continue;
+        }
         if (c < a.dim) {
             const uint64_t e = ((a.list ? a.list[r] : r) + a.row0) * a.dim + c;
             const uint32_t left = (uint32_t)(a.dim - c);
