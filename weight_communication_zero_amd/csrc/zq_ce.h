@@ -208,9 +208,10 @@ hipError_t ce_piece(const CeArgs& a, int w_type, const CeLayout& l, uint32_t v0,
     return launch_stage<T>(s, w_type == kQ8 ? kQ8 : T, stream);
 }
 
-// exp(x), off by about (1 + |x|) 2^-24 of itself.
-__device__ __forceinline__ float exp_of(float x) {
-    return __builtin_amdgcn_exp2f(x * 0x1.715476p0f);
-}
+// Exponentials are taken in base 2: logits times log2(e) are one product of a sum with
+// this factor (rounded once, so that it is off by 2^-24 of each logit).
+__device__ __forceinline__ float base2(float scale) { return scale * 0x1.715476p0f; }
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 }  // namespace zq

@@ -2,8 +2,9 @@
 //
 // The logits of a tile of tokens x vocabulary stay in the matrix product's
 // registers: the epilogue takes each token's maximum m over the tile's columns, the
-// sum s of exp(z - m), and the target's logit where it lies there.  A second kernel
-// joins the tiles' pairs,  (m, s) + (m', s') = (M, s e^(m-M) + s' e^(m'-M)).
+// sum s of 2^(z - m), and the target's logit where it lies there, all of logits in
+// base 2 (times log2 e).  A second kernel joins the tiles' pairs,
+// (m, s) + (m', s') = (M, s 2^(m-M) + s' 2^(m'-M)).
 #include "zq_ce.h"
 
 namespace zq {
@@ -20,7 +21,7 @@ __device__ __forceinline__ float reference(float m) {
 // A pair's sum relative to another reference.  With an infinite maximum the sum is
 // 0, infinity or NaN, and stays so.
 __device__ __forceinline__ float rebased(f2 p, float ref) {
-    return __builtin_fabsf(p.x) < __builtin_inff() ? p.y * exp_of(p.x - ref) : p.y;
+    return __builtin_fabsf(p.x) < __builtin_inff() ? p.y * exp2_of(p.x - ref) : p.y;
 }
 
 struct Stats {
@@ -61,34 +62,46 @@ struct Stats {
             targets[threadIdx.x] = mine.target;
         __syncthreads();
         const uint32_t nw = n0 + wn * (S::BN / S::WN) + (lane >> 4) * 4;
+        const bool whole = n0 + S::BN <= N;
+        const float sign = e.scale < 0.0f ? -1.0f : 1.0f, factor = base2(e.scale) * sign;
 #pragma unroll
         for (int i = 0; i < S::MI; ++i) {
             const uint32_t r = wm * (S::BM / S::WM) + i * 16 + (lane & 15), m = m0 + r;
-            const uint32_t target = m < M && targets[r] < N ? targets[r] : 0xFFFFFFFFu;
-            float top = -__builtin_inff(), z_target = 0.0f;
+            // The largest logit is the largest sum, or with a negative scale the smallest.
+            float top = -__builtin_inff();
 #pragma unroll
             for (int j = 0; j < S::NI; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t n = nw + j * 16 + k;
-                    const float z = e.scale * acc[i][j][k];
-                    acc[i][j][k] = n < N ? z : -__builtin_inff();
-                    if (n < N)
-                        top = __builtin_fmaxf(top, z);
-                    z_target = n == target ? z : z_target;
+                    acc[i][j][k] *= sign;
+                    if (!whole)
+                        acc[i][j][k] =
+                            nw + j * 16 + k < N ? acc[i][j][k] : -__builtin_inff();
+                    top = __builtin_fmaxf(top, acc[i][j][k]);
                 }
-            const uint32_t off = target - nw;
-            if (off < S::NI * 16 && (off & 15) < 4)
-                e.z_target[m] = z_target;
             top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            top = factor * __builtin_fmaxf(top, __shfl_xor(top, 32));
+            // Few waves hold a target of their 16 rows.
+            const uint32_t target = m < M && targets[r] < N ? targets[r] : 0xFFFFFFFFu;
+            const uint32_t off = target - nw;
+            const bool here = off < S::NI * 16 && (off & 15) < 4;
+            if (__builtin_amdgcn_ballot_w64(here)) {
+                float z = 0.0f;
+#pragma unroll
+                for (int j = 0; j < S::NI; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        z = off == j * 16 + k ? acc[i][j][k] : z;
+                if (here)
+                    e.z_target[m] = factor * z;
+            }
             const float ref = reference(top);
             float sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < S::NI; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    sum += exp_of(acc[i][j][k] - ref);
+                    sum += exp2_of(__builtin_fmaf(factor, acc[i][j][k], -ref));
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
             if (lane < 16)
@@ -168,6 +181,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
         a.run[m] = mine;
         return;
     }
+    constexpr float kLn2 = 0x1.62e430p-1f;
     const float ref = reference(mine.x), log_sum = logf(mine.y);
     uint32_t t = m;
     if (a.list) {
@@ -181,8 +195,8 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
             return;
         }
     }
-    a.lse[t] = ref + log_sum;
-    a.loss[t] = (ref - a.z_target[m]) + log_sum;
+    a.lse[t] = __builtin_fmaf(ref, kLn2, log_sum);
+    a.loss[t] = __builtin_fmaf(ref - a.z_target[m], kLn2, log_sum);
 }
 
 // Up to this many tokens the loss is formed for all of them, also those that are left

@@ -282,15 +282,18 @@ __global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi:
 
     const uint32_t base_a = lds_offset(lds), base_b = base_a + D * kA;
     h8 x[2][S::MI], y[2][S::NI];
+    constexpr int kReads = (S::MI + S::NI + S::MI - 1) / S::MI;  // a row of fragments
     auto phase = [&](auto set, uint32_t sa, uint32_t sb, auto half, auto&& issue) {
         constexpr int cur = decltype(set)::value, kk = decltype(half)::value;
 #pragma unroll
         for (int i = 0; i < S::MI; ++i) {
-            x[1 - cur][i] = fa.read(sa, i, kk);
 #pragma unroll
-            for (int j = 0; j < S::NI; ++j)
-                if (j * S::MI / S::NI == i)
-                    y[1 - cur][j] = fb.read(sb, j, kk);
+            for (int r = i * kReads; r < (i + 1) * kReads && r < S::MI + S::NI; ++r) {
+                if (r < S::NI)
+                    y[1 - cur][r < S::NI ? r : 0] = fb.read(sb, r, kk);
+                else
+                    x[1 - cur][r < S::NI ? 0 : r - S::NI] = fa.read(sa, r - S::NI, kk);
+            }
             issue(i);
 #pragma unroll
             for (int j = 0; j < S::NI; ++j)
@@ -386,6 +389,7 @@ __device__ __forceinline__ void mm_rows(f4 (&acc)[S::MI][S::NI], uint32_t wm, ui
                                         uint32_t lane, unsigned char* lds, G&& fetch, F&& put) {
     constexpr int kGroup = S::kGroup;
     constexpr uint32_t kChunks = S::NI * 4;           // of 16 bytes in a row
+    constexpr uint32_t kMask = kChunks < 16 ? kChunks - 1 : 15;
     constexpr uint32_t kAll = kGroup * 16 * kChunks;  // of a wave
     constexpr int kBatch = kAll / 64 < 4 ? kAll / 64 : 4;
     static_assert(kAll % (64 * kBatch) == 0, "whole batches");
@@ -398,7 +402,7 @@ __device__ __forceinline__ void mm_rows(f4 (&acc)[S::MI][S::NI], uint32_t wm, ui
         for (int i = 0; i < kGroup; ++i)
 #pragma unroll
             for (int j = 0; j < S::NI; ++j)
-                *(f4*)(mine + ((i * 16 + r) * kChunks + ((j * 4 + q) ^ (r & (kChunks - 1)))) * 16) =
+                *(f4*)(mine + ((i * 16 + r) * kChunks + ((j * 4 + q) ^ (r & kMask))) * 16) =
                     acc[g * kGroup + i][j];
         wait_lds();
 #pragma unroll 1
@@ -407,7 +411,7 @@ __device__ __forceinline__ void mm_rows(f4 (&acc)[S::MI][S::NI], uint32_t wm, ui
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const uint32_t row = (c0 + k * 64) / kChunks, chunk = (c0 + k * 64) % kChunks;
-                v[k] = *(const f4*)(mine + (row * kChunks + (chunk ^ (row & (kChunks - 1)))) * 16);
+                v[k] = *(const f4*)(mine + (row * kChunks + (chunk ^ (row & kMask))) * 16);
                 old[k] = fetch(mw + g * kGroup * 16 + row, nw + chunk * 4);
             }
 #pragma unroll

@@ -35,23 +35,32 @@ inline uint64_t part_floats(const MmPlan& p, uint64_t M, uint64_t N) {
     return p.splits > 1 ? p.splits * M * round_up(N, 4) : 0;
 }
 
-// The tile and the splits of the least time by a simple model: rounds of workgroups
-// over the CUs, each of its steps and of 4 us around them, and for a split the partial
-// sums' way to memory and back.  What a step of 64 k's takes, measured with all CUs at
-// work: 1.6 us for a 256-tile, 0.95 us for a 128-tile (two of which share a CU), 0.35 us
-// for a small one (two).  A small tile also reads its operands 4 to 8 times as often:
-// with M, N and K large it is never the least.
+// The tile and the splits of the least time by a simple model: the workgroups that a CU
+// works through, each of its steps of 64 k's and of what lies around them, and for a
+// split the partial sums' way to memory and back.  Fitted to measurements; the chosen
+// and the next best of some products, in us (tile edge / splits):
+//   2048 x 2048 x 8192     256/4   76    128/2   93
+//   256 x 4096 x 16384     128/8   53    256/16  62
+//   64 x 4096 x 16384      32/4    35    128/8   41
+//   321 x 515 x 1001       32/1    8.5   128/4   14
+//   64 x 32000 x 2048      32/1    26    128/1   31
+//   300 x 50257 x 768      128/1   41    256/1   49
+//   512 x 32000 x 2048     256/1   61    128/1   77
 inline MmPlan mm_plan(uint64_t M, uint64_t N, uint64_t K, bool may_split) {
-    constexpr double kStepUs[3] = {1.6, 0.95, 0.35};
-    constexpr uint64_t kSlots[3] = {256, 512, 512};
+    struct Cost {
+        double step, around;  // of a workgroup, its CU shared out
+        double alone;         // a step of a workgroup that has a CU to itself
+    };
+    constexpr Cost kCost[3] = {{1.5, 4.0, 1.3}, {0.525, 2.0, 0.9}, {0.175, 2.0, 0.27}};
     const uint64_t steps = std::max<uint64_t>(div_up(K, kMmK), 1);
     MmPlan best = {kTile256, 1};
     double least = 1e30;
     for (int kind : {kTile256, kTile128, kTileSmall}) {
+        const Cost& c = kCost[kind];
         const uint64_t tiles = div_up(M, tile_rows(kind)) * div_up(N, tile_cols(kind));
         for (uint64_t s = 1; s <= (may_split ? kMaxSplits : 1) && (s == 1 || steps / s >= 4); ++s) {
-            const double rounds = (double)div_up(tiles * s, kSlots[kind]);
-            double us = rounds * ((double)div_up(steps, s) * kStepUs[kind] + 4.0);
+            const double per_cu = (double)div_up(tiles * s, 256), n = (double)div_up(steps, s);
+            double us = std::max(per_cu * (n * c.step + c.around), n * c.alone + 4.0);
             if (s > 1)
                 us += 4.0 + (double)(2 * s * M * N) * 4 / 4e6;
             if (us < least) {
