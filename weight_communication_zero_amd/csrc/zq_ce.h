@@ -30,30 +30,31 @@ struct CePrepArgs {
     CeTokens t;
 };
 
-// Gathers the tokens that count.  One workgroup: 2^14 tokens take two rounds (of
-// 8192 ids, 8 a thread, in flight together), and positions need no second pass.
-template <bool GRAD>
+// Gathers the tokens that count.  One workgroup: positions need no second pass, and
+// 2^14 tokens take two rounds of 8192 ids, J = 8 a thread in flight together (J = 1 for
+// 1024 tokens or fewer, whose 7 loads a thread past the end would be for nothing).
+template <bool GRAD, int J>
 __global__ __launch_bounds__(1024) void ce_prep_kernel(CePrepArgs a) {
     __shared__ uint32_t sums[16], maxima[16];
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t count = 0, top = 0;
-    for (uint32_t base = 0; base < a.n_tok; base += 8192) {
-        const uint32_t first = base + wave * 512 + lane;
+    for (uint32_t base = 0; base < a.n_tok; base += 1024 * J) {
+        const uint32_t first = base + wave * (64 * J) + lane;
         const uint32_t last = a.n_tok - 1;
-        uint64_t id[8];
-        load_ids<8>(a.ids, a.id64, [&](int j) { return min(first + j * 64, last); }, id);
-        float lse[8], g[8];
+        uint64_t id[J];
+        load_ids<J>(a.ids, a.id64, [&](int j) { return min(first + j * 64, last); }, id);
+        float lse[J], g[J];
         if constexpr (GRAD) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < J; ++j) {
                 lse[j] = a.lse[min(first + j * 64, last)];
                 g[j] = a.dloss[min(first + j * 64, last)];
             }
         }
-        uint64_t there[8];
+        uint64_t there[J];
         uint32_t mine = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < J; ++j) {
             there[j] = __builtin_amdgcn_ballot_w64(first + j * 64 < a.n_tok && id[j] < a.rows);
             mine += (uint32_t)__builtin_popcountll(there[j]);
         }
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(1024) void ce_prep_kernel(CePrepArgs a) {
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < J; ++j) {
             const uint32_t t = first + j * 64;
             const uint32_t r = at + (uint32_t)__builtin_popcountll(
                                         there[j] & (((uint64_t)1 << lane) - 1));
@@ -166,14 +167,13 @@ template <bool GRAD>
 hipError_t ce_prep(const CeArgs& a, const CeTokens& t, bool scaled, hipStream_t stream) {
     CePrepArgs p = {a.ids, a.id64, a.n_tok, a.rows, scaled, a.lse, a.dloss, a.loss, a.lse_out, t};
     void* args[] = {&p};
-    return hipLaunchKernel((const void*)&ce_prep_kernel<GRAD>, dim3(1), dim3(1024), args, 0,
-                           stream);
+    const void* fn = a.n_tok <= 1024 ? (const void*)&ce_prep_kernel<GRAD, 1>
+                                     : (const void*)&ce_prep_kernel<GRAD, 8>;
+    return hipLaunchKernel(fn, dim3(1), dim3(1024), args, 0, stream);
 }
 
 // The hidden states of the tokens that count, and zeros for dx where one is left out.
-template <int T>
-hipError_t ce_stage_x(const CeArgs& a, const CeLayout& l, const CeTokens& t, char* ws,
-                      hipStream_t stream) {
+inline StageArgs ce_stage_x(const CeArgs& a, const CeLayout& l, const CeTokens& t, char* ws) {
     StageArgs s = {};
     s.src = a.x;
     s.dim = a.dim;
@@ -183,18 +183,23 @@ hipError_t ce_stage_x(const CeArgs& a, const CeLayout& l, const CeTokens& t, cha
     s.list = t.list;
     s.count = &t.scalars->count;
     s.clear = (uint16_t*)a.dx;
-    return launch_stage<T>(s, T, stream);
+    return s;
 }
 
-// Rows v0 .. v0 + n - 1 of the projection as an operand: where they lie, or (codes,
-// widths that are no multiple of 64) staged.
-template <int T>
-hipError_t ce_piece(const CeArgs& a, int w_type, const CeLayout& l, uint32_t v0, uint32_t n,
-                    char* ws, MmOperand* op, hipStream_t stream) {
-    if (w_type != kQ8 && a.dim % kMmK == 0) {
-        *op = {(const uint16_t*)a.w + (uint64_t)v0 * a.dim, a.dim};
-        return hipSuccess;
-    }
+// Whether the projection is an operand where it lies: else (codes, widths that are no
+// multiple of 64) its pieces are staged.
+inline bool w_in_place(const CeArgs& a, int w_type) {
+    return w_type != kQ8 && a.dim % kMmK == 0;
+}
+
+// Rows v0 .. v0 + n - 1 of the projection as an operand.
+inline MmOperand ce_piece(const CeArgs& a, int w_type, const CeLayout& l, uint32_t v0, char* ws) {
+    if (w_in_place(a, w_type))
+        return {(const uint16_t*)a.w + (uint64_t)v0 * a.dim, a.dim};
+    return {(const uint16_t*)(ws + l.w), l.kp};
+}
+
+inline StageArgs ce_stage_w(const CeArgs& a, const CeLayout& l, uint32_t v0, uint32_t n, char* ws) {
     StageArgs s = {};
     s.src = a.w;
     s.scales = a.w_scales;
@@ -204,8 +209,24 @@ hipError_t ce_piece(const CeArgs& a, int w_type, const CeLayout& l, uint32_t v0,
     s.rows = n;
     s.ld = (uint32_t)l.kp;
     s.out = (uint16_t*)(ws + l.w);
-    *op = {s.out, l.kp};
-    return launch_stage<T>(s, w_type == kQ8 ? kQ8 : T, stream);
+    return s;
+}
+
+// Stages what piece i needs: its rows where the projection is not in place, and with the
+// first piece the hidden states where `x` says so.
+template <int T>
+hipError_t ce_stage(const CeArgs& a, int w_type, const CeLayout& l, uint32_t i, bool x,
+                    const CeTokens& t, char* ws, hipStream_t stream) {
+    const uint32_t v0 = i * l.piece;
+    const StageArgs sw = ce_stage_w(a, l, v0, l.rows_of(i, a.rows), ws);
+    const StageArgs sx = ce_stage_x(a, l, t, ws);
+    const bool w = !w_in_place(a, w_type);
+    if (w && x && i == 0)
+        return w_type == kQ8 ? launch_stage_both<T, kQ8, T>(sw, sx, stream)
+                             : launch_stage_both<T, T, T>(sw, sx, stream);
+    if (w)
+        return launch_stage<T>(sw, w_type == kQ8 ? kQ8 : T, stream);
+    return x && i == 0 ? launch_stage<T>(sx, T, stream) : hipSuccess;
 }
 
 // Exponentials are taken in base 2: logits times log2(e) are one product of a sum with

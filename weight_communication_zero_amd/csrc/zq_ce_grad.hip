@@ -96,8 +96,6 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
     char* ws = (char*)a.workspace;
     const CeTokens tok = ce_tokens(l, ws);
     hipError_t st = ce_prep<true>(a, tok, T == kF16, stream);
-    if (st == hipSuccess)
-        st = ce_stage_x<T>(a, l, tok, ws, stream);
     const MmOperand x = {(const uint16_t*)(ws + l.x), l.kp};
     const MmOperand q = {(const uint16_t*)(ws + l.q), l.piece};
     float* acc = (float*)(ws + l.acc);
@@ -105,10 +103,10 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
     const uint32_t* count = &tok.scalars->count;
     for (uint32_t i = 0; i < l.n_pieces && st == hipSuccess; ++i) {
         const uint32_t v0 = i * l.piece, n = l.rows_of(i, a.rows);
-        MmOperand w;
-        st = ce_piece<T>(a, w_type, l, v0, n, ws, &w, stream);
+        st = ce_stage<T>(a, w_type, l, i, true, tok, ws, stream);
         if (st != hipSuccess)
             break;
+        const MmOperand w = ce_piece(a, w_type, l, v0, ws);
         MmArgs m = {};
         m.a = x;
         m.b = w;

@@ -237,14 +237,13 @@ hipError_t launch(const CeArgs& a, int w_type, hipStream_t stream) {
     const bool all = a.n_tok <= kAllTokens && x_in_place(a.n_tok, a.dim);
     hipError_t st = all ? hipSuccess : ce_prep<false>(a, tok, false, stream);
     const uint32_t* count = all ? nullptr : &tok.scalars->count;
-    if (st == hipSuccess && !x_in_place(a.n_tok, a.dim))
-        st = ce_stage_x<T>(a, l, tok, ws, stream);
     for (uint32_t i = 0; i < l.n_pieces && st == hipSuccess; ++i) {
         const uint32_t v0 = i * l.piece, n = l.rows_of(i, a.rows);
         MmArgs m = {};
-        st = ce_piece<T>(a, w_type, l, v0, n, ws, &m.b, stream);
+        st = ce_stage<T>(a, w_type, l, i, !x_in_place(a.n_tok, a.dim), tok, ws, stream);
         if (st != hipSuccess)
             break;
+        m.b = ce_piece(a, w_type, l, v0, ws);
         m.a = {(const uint16_t*)(ws + l.x), l.kp};
         if (x_in_place(a.n_tok, a.dim)) {
             m.a.p = (const uint16_t*)a.x;

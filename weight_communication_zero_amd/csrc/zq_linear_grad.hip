@@ -48,22 +48,23 @@ hipError_t launch(const LinearGradArgs& a, int grad_type, int mode, hipStream_t 
     s.rows = a.n_tok;
     s.ld = (uint32_t)l.ldx;
     s.out = (uint16_t*)(ws + l.x);
-    hipError_t st = launch_stage<T>(s, kQ8, stream);
-    if (st != hipSuccess)
-        return st;
     MmArgs m = {};
     m.a = {(const uint16_t*)a.dy, a.out_dim};
+    hipError_t st;
     if (l.stage_dy) {
-        s.src = a.dy;
-        s.scales = nullptr;
-        s.dim = a.out_dim;
-        s.ld = (uint32_t)l.ldy;
-        s.out = (uint16_t*)(ws + l.dy);
-        st = launch_stage<T>(s, T, stream);
-        if (st != hipSuccess)
-            return st;
-        m.a = {s.out, l.ldy};
+        StageArgs d = {};
+        d.src = a.dy;
+        d.dim = a.out_dim;
+        d.rows = a.n_tok;
+        d.ld = (uint32_t)l.ldy;
+        d.out = (uint16_t*)(ws + l.dy);
+        m.a = {d.out, l.ldy};
+        st = launch_stage_both<T, kQ8, T>(s, d, stream);
+    } else {
+        st = launch_stage<T>(s, kQ8, stream);
     }
+    if (st != hipSuccess)
+        return st;
     m.b = {(const uint16_t*)(ws + l.x), l.ldx};
     m.M = a.out_dim;
     m.N = a.in_dim;

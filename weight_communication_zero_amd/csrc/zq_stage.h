@@ -21,13 +21,13 @@ struct StageArgs {
                             // are cleared in it
 };
 
-// A lane per group of 8 elements of the result.
+// A lane per group of 8 elements of the result; the calling workgroup is wg of wgs.
 template <int T, int IN, bool WHOLE>
-__global__ __launch_bounds__(256) void stage_kernel(StageArgs a) {
+__device__ __forceinline__ void stage_rows(const StageArgs& a, uint32_t wg, uint32_t wgs) {
     const uint32_t rows = a.count ? min(a.rows, *a.count) : a.rows;
     const uint32_t per_row = a.ld / 8;
     const uint64_t groups = (uint64_t)(a.clear ? a.rows : rows) * per_row;
-    for (uint64_t g = blockIdx.x * 256ull + threadIdx.x; g < groups; g += gridDim.x * 256ull) {
+    for (uint64_t g = wg * 256ull + threadIdx.x; g < groups; g += wgs * 256ull) {
         const uint32_t r = (uint32_t)(g / per_row);
         const uint32_t c = (uint32_t)(g - (uint64_t)r * per_row) * 8;
         Raw<T, 8> v = {{0, 0, 0, 0}};
@@ -65,6 +65,16 @@ __global__ __launch_bounds__(256) void stage_kernel(StageArgs a) {
     }
 }
 
+template <int T, int IN, bool WHOLE>
+__global__ __launch_bounds__(256) void stage_kernel(StageArgs a) {
+    stage_rows<T, IN, WHOLE>(a, blockIdx.x, gridDim.x);
+}
+
+inline uint32_t stage_wgs(const StageArgs& a) {
+    const uint64_t wgs = ((uint64_t)a.rows * (a.ld / 8) + 255) / 256;
+    return (uint32_t)(wgs < 65536 ? wgs : 65536);
+}
+
 // in: T, or kQ8.
 template <int T>
 hipError_t launch_stage(const StageArgs& a, int in, hipStream_t stream) {
@@ -77,9 +87,31 @@ hipError_t launch_stage(const StageArgs& a, int in, hipStream_t stream) {
                                : (const void*)&stage_kernel<T, T, false>;
     StageArgs k = a;
     void* args[] = {&k};
-    const uint64_t wgs = ((uint64_t)a.rows * (a.ld / 8) + 255) / 256;
-    return hipLaunchKernel(fn, dim3((uint32_t)(wgs < 65536 ? wgs : 65536)), dim3(256), args, 0,
-                           stream);
+    return hipLaunchKernel(fn, dim3(stage_wgs(a)), dim3(256), args, 0, stream);
+}
+
+// Two operands in one launch: the first by the first `wgs` workgroups.
+template <int T, int IN1, bool WHOLE1, int IN2, bool WHOLE2>
+__global__ __launch_bounds__(256) void stage_both_kernel(StageArgs a, StageArgs b, uint32_t wgs) {
+    if (blockIdx.x < wgs)
+        stage_rows<T, IN1, WHOLE1>(a, blockIdx.x, wgs);
+    else
+        stage_rows<T, IN2, WHOLE2>(b, blockIdx.x - wgs, gridDim.x - wgs);
+}
+
+// a of type IN1 (T or kQ8), b of type IN2.
+template <int T, int IN1, int IN2>
+hipError_t launch_stage_both(const StageArgs& a, const StageArgs& b, hipStream_t stream) {
+    const bool wa = a.dim % 8 == 0, wb = b.dim % 8 == 0;
+    const void* fn =
+        wa   ? wb ? (const void*)&stage_both_kernel<T, IN1, true, IN2, true>
+                  : (const void*)&stage_both_kernel<T, IN1, true, IN2, false>
+        : wb ? (const void*)&stage_both_kernel<T, IN1, false, IN2, true>
+             : (const void*)&stage_both_kernel<T, IN1, false, IN2, false>;
+    StageArgs ka = a, kb = b;
+    uint32_t wgs = stage_wgs(a);
+    void* args[] = {&ka, &kb, &wgs};
+    return hipLaunchKernel(fn, dim3(wgs + stage_wgs(b)), dim3(256), args, 0, stream);
 }
 
 }  // namespace zq

@@ -572,21 +572,38 @@ def _blocks(n: int, block: int) -> int:
     return (n + block - 1) // block if block > 0 else 0
 
 
+def _fits(t, dtype, n: int, device: int) -> bool:
+    """_need's checks of one dtype in four attribute reads."""
+    return (t.__class__ is not int and t.get_device() == device and t.dtype is dtype
+            and t.numel() >= n and t.is_contiguous())
+
+
+def _current(t) -> int:
+    """The device of t where that is the current one, else a number of no device."""
+    dev = t.get_device()
+    return dev if dev >= 0 and dev == _device() else -2
+
+
 def zq_swiglu_int8(gate, up, block: int, h, gate_codes, gate_scales, up_codes, up_scales,
                    stream=None) -> None:
     """h = gate * sigmoid(gate) * up (fp32/bf16/fp16, all of one dtype), and gate
     and up as zq_quant_int8 blocks for zq_swiglu_grad_int8."""
-    n = gate.numel()
-    _need("gate", gate, n, _FLOAT)
-    _need("up", up, n, (gate.dtype,))
-    _need("h", h, n, (gate.dtype,))
-    _need("gate_codes", gate_codes, n, _I8)
-    _need("gate_scales", gate_scales, _blocks(n, block), _F32)
-    _need("up_codes", up_codes, n, _I8)
-    _need("up_scales", up_scales, _blocks(n, block), _F32)
+    n, dt, dev, nb = gate.numel(), gate.dtype, _current(gate), _blocks(gate.numel(), block)
+    ptr = torch.Tensor.data_ptr
+    if not (_fits(gate, dt, n, dev) and _fits(up, dt, n, dev) and _fits(h, dt, n, dev)
+            and _fits(gate_codes, torch.int8, n, dev) and _fits(up_codes, torch.int8, n, dev)
+            and _fits(gate_scales, torch.float32, nb, dev)
+            and _fits(up_scales, torch.float32, nb, dev)):
+        for name, t, m, dtypes in (("gate", gate, n, _FLOAT), ("up", up, n, (dt,)),
+                                   ("h", h, n, (dt,)), ("gate_codes", gate_codes, n, _I8),
+                                   ("gate_scales", gate_scales, nb, _F32),
+                                   ("up_codes", up_codes, n, _I8),
+                                   ("up_scales", up_scales, nb, _F32)):
+            _need(name, t, m, dtypes)
+        ptr = _p
     _check("zq_swiglu_int8",
-           lib.zq_swiglu_int8(_p(gate), _p(up), _dtype(gate), n, block, _p(h), _p(gate_codes),
-                              _p(gate_scales), _p(up_codes), _p(up_scales), _stream(stream)))
+           lib.zq_swiglu_int8(ptr(gate), ptr(up), _dtype(gate), n, block, ptr(h), ptr(gate_codes),
+                              ptr(gate_scales), ptr(up_codes), ptr(up_scales), _stream(stream)))
 
 
 def zq_swiglu_grad_int8(gate_codes, gate_scales, up_codes, up_scales, block: int, dh, dgate, dup,
@@ -594,19 +611,24 @@ def zq_swiglu_grad_int8(gate_codes, gate_scales, up_codes, up_scales, block: int
     """dgate and dup of zq_swiglu_int8 at its kept values, for h's gradient dh
     (fp32/bf16/fp16, all of one dtype); h, where given, gets the product of the
     kept values."""
-    n = dh.numel()
-    _need("gate_codes", gate_codes, n, _I8)
-    _need("gate_scales", gate_scales, _blocks(n, block), _F32)
-    _need("up_codes", up_codes, n, _I8)
-    _need("up_scales", up_scales, _blocks(n, block), _F32)
-    _need("dh", dh, n, _FLOAT)
-    _need("dgate", dgate, n, (dh.dtype,))
-    _need("dup", dup, n, (dh.dtype,))
-    _need("h", h, n, (dh.dtype,))
+    n, dt, dev, nb = dh.numel(), dh.dtype, _current(dh), _blocks(dh.numel(), block)
+    ptr = torch.Tensor.data_ptr
+    if not (_fits(dh, dt, n, dev) and _fits(dgate, dt, n, dev) and _fits(dup, dt, n, dev)
+            and (h is None or _fits(h, dt, n, dev)) and _fits(gate_codes, torch.int8, n, dev)
+            and _fits(up_codes, torch.int8, n, dev) and _fits(gate_scales, torch.float32, nb, dev)
+            and _fits(up_scales, torch.float32, nb, dev)):
+        for name, t, m, dtypes in (("gate_codes", gate_codes, n, _I8),
+                                   ("gate_scales", gate_scales, nb, _F32),
+                                   ("up_codes", up_codes, n, _I8),
+                                   ("up_scales", up_scales, nb, _F32), ("dh", dh, n, _FLOAT),
+                                   ("dgate", dgate, n, (dt,)), ("dup", dup, n, (dt,)),
+                                   ("h", h, n, (dt,))):
+            _need(name, t, m, dtypes)
+        ptr = _p
     _check("zq_swiglu_grad_int8",
-           lib.zq_swiglu_grad_int8(_p(gate_codes), _p(gate_scales), _p(up_codes), _p(up_scales),
-                                   block, _p(dh), _dtype(dh), n, _p(dgate), _p(dup), _p(h),
-                                   _stream(stream)))
+           lib.zq_swiglu_grad_int8(ptr(gate_codes), ptr(gate_scales), ptr(up_codes),
+                                   ptr(up_scales), block, ptr(dh), _dtype(dh), n, ptr(dgate),
+                                   ptr(dup), None if h is None else ptr(h), _stream(stream)))
 
 
 def linear_grad_workspace(n_tok: int, out_dim: int, in_dim: int) -> int:
