@@ -223,8 +223,11 @@ struct MmInt {
 // so that the matrix units wait neither for LDS nor for the loads' issue (all loads
 // of a step behind its barrier, and all reads before its products, took 3.45 and 3.56
 // ms for 16384 x 32000 x 4096 in bf16; this order takes 3.20, 1340 TFLOP/s).
+//
+// Two waves a SIMD are asked for (LDS lets no more in): with 512 registers to give, the
+// compiler would keep the sums in accumulation registers and move fragments to and fro.
 template <class S, class Epi>
-__global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi::Args e) {
+__global__ __launch_bounds__(S::kThreads, 2) void mm_kernel(MmArgs a, typename Epi::Args e) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[S::kLds];
     using TileA = MmTile<S::BM, S::TA, S::kWaves>;
     using TileB = MmTile<S::BN, S::TB, S::kWaves>;
@@ -335,14 +338,14 @@ __global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi:
             y[0][j] = fb.read(base_b, j, 0);
     }
     uint32_t oa = 0, ob = 0, ob_new = D * kB;  // stages of step s, and of step s + D of b
-    for (uint32_t s = 0; s < steps; ++s) {
-        const bool more = s + D < steps;
+    auto step = [&](uint32_t s, auto more) {
+        constexpr bool kMore = decltype(more)::value;  // step s + D is there to load
         const uint32_t left = count - (s + D) * kMmK;
         const uint32_t oa1 = oa == (D - 1) * kA ? 0 : oa + kA, ob1 = ob == D * kB ? 0 : ob + kB;
         const i4v srd_a = buffer_of(pa), srd_b = buffer_of(pb);
         __builtin_amdgcn_sched_barrier(0);
         phase(MmInt<0>(), base_a + oa, base_b + ob, MmInt<1>(), [&](int i) {
-            if (more)
+            if constexpr (kMore)
 #pragma unroll
                 for (int j = 0; j < kLoadsB; ++j)
                     if (j * S::MI / kLoadsB == i)
@@ -351,15 +354,16 @@ __global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi:
         // Past step s + 1's loads, those of steps s + 2 to s + D - 1 and the ones just
         // issued may be under way.
         wait_lds();
-        if (more)
+        if constexpr (kMore)
             wait_vm<(D - 2) * (kLoadsA + kLoadsB) + kLoadsB>();
         else
             wait_vm<0>();
         __builtin_amdgcn_s_barrier();
-        clear(s + 1, oa1, ob1);
+        if constexpr (!kMore)
+            clear(s + 1, oa1, ob1);
         __builtin_amdgcn_sched_barrier(0);
         phase(MmInt<1>(), base_a + oa1, base_b + ob1, MmInt<0>(), [&](int i) {
-            if (more)
+            if constexpr (kMore)
 #pragma unroll
                 for (int j = 0; j < kLoadsA; ++j)
                     if (j * S::MI / (2 * kLoadsA) == i)
@@ -370,7 +374,12 @@ __global__ __launch_bounds__(S::kThreads) void mm_kernel(MmArgs a, typename Epi:
         oa = oa1;
         ob_new = ob;
         ob = ob1;
-    }
+    };
+    uint32_t s = 0;
+    for (; s + D < steps; ++s)
+        step(s, MmInt<1>());
+    for (; s < steps; ++s)
+        step(s, MmInt<0>());
     wait_lds();
     __builtin_amdgcn_s_barrier();
     // acc[i][j][r] is C at m = m0 + wm BM / WM + 16 i + (lane & 15),

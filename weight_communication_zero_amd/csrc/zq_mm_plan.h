@@ -39,19 +39,18 @@ inline uint64_t part_floats(const MmPlan& p, uint64_t M, uint64_t N) {
 // works through, each of its steps of 64 k's and of what lies around them, and for a
 // split the partial sums' way to memory and back.  Fitted to measurements; the chosen
 // and the next best of some products, in us (tile edge / splits):
-//   2048 x 2048 x 8192     256/4   76    128/2   93
-//   256 x 4096 x 16384     128/8   53    256/16  62
-//   64 x 4096 x 16384      32/4    35    128/8   41
-//   321 x 515 x 1001       32/1    8.5   128/4   14
-//   64 x 32000 x 2048      32/1    26    128/1   31
-//   300 x 50257 x 768      128/1   41    256/1   49
-//   512 x 32000 x 2048     256/1   61    128/1   77
+//   2048 x 2048 x 8192     128/2   73    256/4   75
+//   256 x 4096 x 16384     128/8   49    256/8   60
+//   321 x 515 x 1001       32/1    7.3   128/4   12
+//   65 x 513 x 1000        32/1    6.6   128/4   11
+//   256 x 32000 x 2048     128/1   37    256/1   50
+//   512 x 32000 x 2048     256/1   59    128/1   67
 inline MmPlan mm_plan(uint64_t M, uint64_t N, uint64_t K, bool may_split) {
     struct Cost {
         double step, around;  // of a workgroup, its CU shared out
         double alone;         // a step of a workgroup that has a CU to itself
     };
-    constexpr Cost kCost[3] = {{1.5, 4.0, 1.3}, {0.525, 2.0, 0.9}, {0.175, 2.0, 0.27}};
+    constexpr Cost kCost[3] = {{1.5, 4.0, 1.25}, {0.475, 2.0, 0.62}, {0.185, 2.0, 0.19}};
     const uint64_t steps = std::max<uint64_t>(div_up(K, kMmK), 1);
     MmPlan best = {kTile256, 1};
     double least = 1e30;
@@ -62,7 +61,7 @@ inline MmPlan mm_plan(uint64_t M, uint64_t N, uint64_t K, bool may_split) {
             const double per_cu = (double)div_up(tiles * s, 256), n = (double)div_up(steps, s);
             double us = std::max(per_cu * (n * c.step + c.around), n * c.alone + 4.0);
             if (s > 1)
-                us += 4.0 + (double)(2 * s * M * N) * 4 / 4e6;
+                us += 3.0 + (double)(2 * s * M * N) * 4 / 5e6;
             if (us < least) {
                 least = us;
                 best = {kind, (uint32_t)s};
