@@ -121,7 +121,7 @@ struct CeLayout {
     MmPlan logits;
     uint64_t scalars, list, target, lse, dloss, x, w;
     uint64_t part, run, z_target;   // loss
-    uint64_t q, acc, sums;          // gradient
+    uint64_t q, acc, x_sums, w_sums;  // gradient
     uint64_t ldacc;
     uint64_t total;
 

@@ -35,8 +35,9 @@ struct Residual {
     template <class S>
     static __device__ __forceinline__ void finish(const Args& e, const Row& mine,
                                                   f4 (&acc)[S::MI][S::NI], uint32_t M, uint32_t N,
-                                                  uint32_t m0, uint32_t n0, uint32_t wm,
-                                                  uint32_t wn, uint32_t lane, unsigned char* lds) {
+                                                  uint32_t m0, uint32_t n0, uint32_t,
+                                                  uint32_t wm, uint32_t wn, uint32_t lane,
+                                                  unsigned char* lds) {
         // The rows' values behind the part of LDS that the sums go through.
         static_assert(S::kThreads >= S::BM && S::kRowsLds + S::BM * sizeof(Row) <= S::kLds, "fits");
         Row* rows = (Row*)(lds + S::kRowsLds);
@@ -80,12 +81,13 @@ CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
     l.q = take((uint64_t)n_tok * l.piece * 2);
     l.ldacc = round_up(dim, 4);
     l.acc = take(l.n_pieces > 1 ? n_tok * l.ldacc * 4 : 0);
-    uint64_t floats = 0;
+    uint64_t x_floats = 0, w_floats = 0;
     for (uint32_t n : {l.piece, l.rows_of(l.n_pieces - 1, rows)}) {
-        floats = std::max(floats, part_floats(mm_plan(n_tok, dim, n, true), n_tok, dim));
-        floats = std::max(floats, part_floats(mm_plan(n, dim, n_tok, true), n, dim));
+        x_floats = std::max(x_floats, part_floats(mm_plan(n_tok, dim, n, true), n_tok, dim));
+        w_floats = std::max(w_floats, part_floats(mm_plan(n, dim, n_tok, true), n, dim));
     }
-    l.sums = take(floats * 4);
+    l.x_sums = take(x_floats * 4);
+    l.w_sums = take(w_floats * 4);
     l.total = take.at;
     return l;
 }
@@ -99,7 +101,6 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
     const MmOperand x = {(const uint16_t*)(ws + l.x), l.kp};
     const MmOperand q = {(const uint16_t*)(ws + l.q), l.piece};
     float* acc = (float*)(ws + l.acc);
-    float* sums = (float*)(ws + l.sums);
     const uint32_t* count = &tok.scalars->count;
     for (uint32_t i = 0; i < l.n_pieces && st == hipSuccess; ++i) {
         const uint32_t v0 = i * l.piece, n = l.rows_of(i, a.rows);
@@ -116,41 +117,41 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
         m.dyn_m = count;
         Residual::Args e = {a.scale, (uint16_t*)(ws + l.q), l.piece, tok, v0};
         st = launch_mm<T, false, false, Residual>(m, e, l.logits, stream);
+        if (st != hipSuccess)
+            break;
         MmOut o = {};
         o.ldacc = l.ldacc;
         o.ldo = a.dim;
         o.factor = &tok.scalars->down;
         o.scale = a.scale;
-        if (st == hipSuccess && a.dx) {
-            m.a = q;
-            m.N = a.dim;
-            m.K = n;
-            m.b_cols = (uint32_t)l.kp;
-            MmOut d = o;
-            d.acc_in = i ? acc : nullptr;
-            d.acc_out = i + 1 < l.n_pieces ? acc : nullptr;
-            d.out = a.dx;
-            d.list = tok.list;
-            d.type = T;
-            st = launch_mm_sum<T, false, true>(m, d, mm_plan(a.n_tok, a.dim, n, true), sums,
-                                               stream);
-        }
-        if (st == hipSuccess && a.dw) {
-            MmArgs g = {};
-            g.a = q;
-            g.b = x;
-            g.M = n;
-            g.N = a.dim;
-            g.K = a.n_tok;
-            g.a_cols = l.piece;
-            g.b_cols = (uint32_t)l.kp;
-            g.dyn_k = count;
-            MmOut d = o;
-            d.out = (char*)a.dw + (uint64_t)v0 * a.dim * (dw_type == kF32 ? 4 : 2);
-            d.type = dw_type;
-            d.add = mode == kGradAdd;
-            st = launch_mm_sum<T, true, true>(g, d, mm_plan(n, a.dim, a.n_tok, true), sums, stream);
-        }
+        MmInto to_x = {m, o, mm_plan(a.n_tok, a.dim, n, true), (float*)(ws + l.x_sums)};
+        to_x.a.a = q;
+        to_x.a.N = a.dim;
+        to_x.a.K = n;
+        to_x.a.b_cols = (uint32_t)l.kp;
+        to_x.o.acc_in = i ? acc : nullptr;
+        to_x.o.acc_out = i + 1 < l.n_pieces ? acc : nullptr;
+        to_x.o.out = a.dx;
+        to_x.o.list = tok.list;
+        to_x.o.type = T;
+        MmInto to_w = {{}, o, mm_plan(n, a.dim, a.n_tok, true), (float*)(ws + l.w_sums)};
+        to_w.a.a = q;
+        to_w.a.b = x;
+        to_w.a.M = n;
+        to_w.a.N = a.dim;
+        to_w.a.K = a.n_tok;
+        to_w.a.a_cols = l.piece;
+        to_w.a.b_cols = (uint32_t)l.kp;
+        to_w.a.dyn_k = count;
+        to_w.o.out = (char*)a.dw + (uint64_t)v0 * a.dim * (dw_type == kF32 ? 4 : 2);
+        to_w.o.type = dw_type;
+        to_w.o.add = mode == kGradAdd;
+        if (a.dx && a.dw)
+            st = launch_mm_two_sums<T>(to_x, to_w, stream);
+        else if (a.dx)
+            st = launch_mm_sum<T, false, true>(to_x, stream);
+        else
+            st = launch_mm_sum<T, true, true>(to_w, stream);
     }
     return st;
 }

@@ -53,8 +53,9 @@ struct Stats {
     template <class S>
     static __device__ __forceinline__ void finish(const Args& e, const Row& mine,
                                                   f4 (&acc)[S::MI][S::NI], uint32_t M, uint32_t N,
-                                                  uint32_t m0, uint32_t n0, uint32_t wm,
-                                                  uint32_t wn, uint32_t lane, unsigned char* lds) {
+                                                  uint32_t m0, uint32_t n0, uint32_t,
+                                                  uint32_t wm, uint32_t wn, uint32_t lane,
+                                                  unsigned char* lds) {
         f2* pair = (f2*)lds;                              // [WN][BM]
         uint32_t* targets = (uint32_t*)(pair + S::WN * S::BM);  // [BM]
         static_assert(S::kThreads >= S::BM && S::BM * (8 * S::WN + 4) <= S::kLds, "fits");

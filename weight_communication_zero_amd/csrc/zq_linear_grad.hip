@@ -77,7 +77,7 @@ hipError_t launch(const LinearGradArgs& a, int grad_type, int mode, hipStream_t 
     o.scale = 1.0f;
     o.type = grad_type;
     o.add = mode == kGradAdd;
-    return launch_mm_sum<T, true, true>(m, o, l.plan, (float*)(ws + l.part), stream);
+    return launch_mm_sum<T, true, true>({m, o, l.plan, (float*)(ws + l.part)}, stream);
 }
 
 }  // namespace

@@ -30,6 +30,8 @@ struct MmArgs {
                                // (all of them within 4 GiB)
     const uint32_t* dyn_m;     // where set, M (K) is the smaller of M (K) and this
     const uint32_t* dyn_k;
+    uint32_t wgs, splits;      // workgroups of a split (a multiple of 8, one for each
+                               // tile or more); parts that the k's are split into
 };
 
 typedef __attribute__((address_space(3))) unsigned char lds_byte;
@@ -51,6 +53,9 @@ __device__ __forceinline__ i4v buffer_of(const void* p) {
     const uint64_t a = (uint64_t)(uintptr_t)p;
     i4v r = {(int)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
              (int)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)), -1, 0x00020000};
+    // Should a vector instruction have written the words, a load that reads them has to
+    // stay 5 cycles behind; the compiler does not see the loads in dma16.
+    asm volatile("s_nop 4" : "+s"(r));
     return r;
 }
 
@@ -223,12 +228,9 @@ struct MmInt {
 // so that the matrix units wait neither for LDS nor for the loads' issue (all loads
 // of a step behind its barrier, and all reads before its products, took 3.45 and 3.56
 // ms for 16384 x 32000 x 4096 in bf16; this order takes 3.20, 1340 TFLOP/s).
-//
-// Two waves a SIMD are asked for (LDS lets no more in): with 512 registers to give, the
-// compiler would keep the sums in accumulation registers and move fragments to and fro.
 template <class S, class Epi>
-__global__ __launch_bounds__(S::kThreads, 2) void mm_kernel(MmArgs a, typename Epi::Args e) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[S::kLds];
+__device__ __forceinline__ void mm_run(const MmArgs& a, const typename Epi::Args& e, uint32_t wg,
+                                       unsigned char* lds) {
     using TileA = MmTile<S::BM, S::TA, S::kWaves>;
     using TileB = MmTile<S::BN, S::TB, S::kWaves>;
     constexpr uint32_t kA = TileA::kBytes, kB = TileB::kBytes;
@@ -242,11 +244,13 @@ __global__ __launch_bounds__(S::kThreads, 2) void mm_kernel(MmArgs a, typename E
         M = min(M, *a.dyn_m);
     if (a.dyn_k)
         K = min(K, *a.dyn_k);
+    const uint32_t split = wg / a.wgs;
+    wg -= split * a.wgs;
     // Workgroup b runs on XCD b % 8: each XCD takes an eighth of the tiles in a row.
     const uint32_t tm = (M + S::BM - 1) / S::BM, tn = (a.N + S::BN - 1) / S::BN;
     const uint32_t total = tm * tn, per = (total + 7) / 8;
-    const uint32_t t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || t >= total)
+    const uint32_t t = (wg & 7) * per + (wg >> 3);
+    if ((wg >> 3) >= per || t >= total)
         return;
     uint32_t im, in;
     mm_tile_of(t, tm, tn, &im, &in);
@@ -254,8 +258,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void mm_kernel(MmArgs a, typename E
 
     // This split's k's.
     const uint32_t steps_all = (K + kMmK - 1) / kMmK;
-    const uint32_t per_split = (steps_all + gridDim.y - 1) / gridDim.y;
-    const uint32_t s0 = min(blockIdx.y * per_split, steps_all);
+    const uint32_t per_split = (steps_all + a.splits - 1) / a.splits;
+    const uint32_t s0 = min(split * per_split, steps_all);
     const uint32_t steps = min(per_split, steps_all - s0);
     const uint32_t count = K - s0 * kMmK;  // k's from the split's first on
 
@@ -384,7 +388,30 @@ __global__ __launch_bounds__(S::kThreads, 2) void mm_kernel(MmArgs a, typename E
     __builtin_amdgcn_s_barrier();
     // acc[i][j][r] is C at m = m0 + wm BM / WM + 16 i + (lane & 15),
     // n = n0 + wn BN / WN + 16 j + 4 (lane >> 4) + r.
-    Epi::template finish<S>(e, row, acc, M, a.N, m0, n0, wm, wn, lane, lds);
+    Epi::template finish<S>(e, row, acc, M, a.N, m0, n0, split, wm, wn, lane, lds);
+}
+
+// Two waves a SIMD are asked for (LDS lets no more in): with 512 registers to give, the
+// compiler would keep the sums in accumulation registers and move fragments to and fro.
+template <class S, class Epi>
+__global__ __launch_bounds__(S::kThreads, 2) void mm_kernel(MmArgs a, typename Epi::Args e) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[S::kLds];
+    mm_run<S, Epi>(a, e, blockIdx.x, lds);
+}
+
+// Two products in one launch, so that the second's tiles fill the CUs that the first's
+// last ones leave idle.
+template <class S1, class S2, class Epi>
+__global__ __launch_bounds__(S1::kThreads, 2) void mm_pair_kernel(MmArgs a1, typename Epi::Args e1,
+                                                                  MmArgs a2,
+                                                                  typename Epi::Args e2) {
+    static_assert(S1::kThreads == S2::kThreads && S1::kLds == S2::kLds, "tiles of one kind");
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[S1::kLds];
+    const uint32_t first = a1.wgs * a1.splits;
+    if (blockIdx.x < first)
+        mm_run<S1, Epi>(a1, e1, blockIdx.x, lds);
+    else
+        mm_run<S2, Epi>(a2, e2, blockIdx.x - first, lds);
 }
 
 // Hands each f4 of a wave's sums to put(m in the tile, n in the tile, f4, what
@@ -533,7 +560,7 @@ struct MmOut {
     }
 };
 
-// The epilogue of sums: put, or with part set (K split over gridDim.y) the split's
+// The epilogue of sums: put, or with part set (K is split) the split's
 // partial sums at part[(split * rows + m) * ld + n], for mm_join_kernel.
 struct MmSum {
     struct Args {
@@ -548,8 +575,9 @@ struct MmSum {
     template <class S>
     static __device__ __forceinline__ void finish(const Args& e, const Row&,
                                                   f4 (&acc)[S::MI][S::NI], uint32_t M, uint32_t N,
-                                                  uint32_t m0, uint32_t n0, uint32_t wm,
-                                                  uint32_t wn, uint32_t lane, unsigned char* lds) {
+                                                  uint32_t m0, uint32_t n0, uint32_t split,
+                                                  uint32_t wm, uint32_t wn, uint32_t lane,
+                                                  unsigned char* lds) {
         const bool part = e.part != nullptr;
         mm_rows<S>(
             acc, wm, wn, lane, lds,
@@ -562,7 +590,7 @@ struct MmSum {
                 if (m >= M || n >= N)
                     return;
                 if (part)
-                    *(f4*)(e.part + (blockIdx.y * e.rows + m) * e.ld + n) = v;
+                    *(f4*)(e.part + (split * e.rows + m) * e.ld + n) = v;
                 else
                     e.o.put(m, n, N - n, v, old);
             });

@@ -71,42 +71,87 @@ inline MmPlan mm_plan(uint64_t M, uint64_t N, uint64_t K, bool may_split) {
     return best;
 }
 
-template <class S, class Epi>
-hipError_t launch_mm_shape(const MmArgs& a, const typename Epi::Args& e, uint32_t splits,
-                           hipStream_t stream) {
-    const uint64_t tiles = div_up(a.M, S::BM) * div_up(a.N, S::BN);
-    MmArgs k = a;
-    typename Epi::Args ke = e;
-    void* args[] = {&k, &ke};
-    return hipLaunchKernel((const void*)&mm_kernel<S, Epi>,
-                           dim3((uint32_t)div_up(tiles, 8) * 8, splits), dim3(S::kThreads), args, 0,
-                           stream);
+template <int T, bool TA, bool TB>
+using MmShape256 = MmShape<T, 256, 256, 2, 4, 2, TA, TB>;
+template <int T, bool TA, bool TB>
+using MmShape128 = MmShape<T, 128, 128, 2, 2, 2, TA, TB>;
+template <int T, bool TA, bool TB>
+using MmShapeSmall = MmShape<T, 32, 64, 1, 4, 4, TA, TB>;
+
+constexpr uint32_t tile_threads(int kind) { return kind == kTile256 ? 512 : 256; }
+
+// The product with its plan's grid.
+inline MmArgs mm_planned(MmArgs a, const MmPlan& p) {
+    a.wgs = (uint32_t)div_up(div_up(a.M, tile_rows(p.kind)) * div_up(a.N, tile_cols(p.kind)), 8) * 8;
+    a.splits = p.splits;
+    return a;
 }
 
 template <int T, bool TA, bool TB, class Epi>
 hipError_t launch_mm(const MmArgs& a, const typename Epi::Args& e, const MmPlan& p,
                      hipStream_t stream) {
-    if (p.kind == kTile256)
-        return launch_mm_shape<MmShape<T, 256, 256, 2, 4, 2, TA, TB>, Epi>(a, e, p.splits, stream);
-    if (p.kind == kTile128)
-        return launch_mm_shape<MmShape<T, 128, 128, 2, 2, 2, TA, TB>, Epi>(a, e, p.splits, stream);
-    return launch_mm_shape<MmShape<T, 32, 64, 1, 4, 4, TA, TB>, Epi>(a, e, p.splits, stream);
+    const void* fn = p.kind == kTile256   ? (const void*)&mm_kernel<MmShape256<T, TA, TB>, Epi>
+                     : p.kind == kTile128 ? (const void*)&mm_kernel<MmShape128<T, TA, TB>, Epi>
+                                          : (const void*)&mm_kernel<MmShapeSmall<T, TA, TB>, Epi>;
+    MmArgs k = mm_planned(a, p);
+    typename Epi::Args ke = e;
+    void* args[] = {&k, &ke};
+    return hipLaunchKernel(fn, dim3(k.wgs * k.splits), dim3(tile_threads(p.kind)), args, 0, stream);
 }
 
 // A product into MmOut, its partial sums (where split) in `part`.
-template <int T, bool TA, bool TB>
-hipError_t launch_mm_sum(const MmArgs& a, const MmOut& o, const MmPlan& p, float* part,
-                         hipStream_t stream) {
-    MmSum::Args e = {o, p.splits > 1 ? part : nullptr, a.M, round_up(a.N, 4)};
-    hipError_t st = launch_mm<T, TA, TB, MmSum>(a, e, p, stream);
-    if (st != hipSuccess || p.splits == 1)
-        return st;
-    uint32_t splits = p.splits, M = a.M, N = a.N;
-    const uint32_t* dyn = a.dyn_m;
+struct MmInto {
+    MmArgs a;
+    MmOut o;
+    MmPlan plan;
+    float* part;
+
+    MmSum::Args sum() const {
+        return {o, plan.splits > 1 ? part : nullptr, a.M, round_up(a.N, 4)};
+    }
+};
+
+inline hipError_t launch_mm_join(const MmInto& p, hipStream_t stream) {
+    if (p.plan.splits == 1)
+        return hipSuccess;
+    MmSum::Args e = p.sum();
+    uint32_t splits = p.plan.splits, M = p.a.M, N = p.a.N;
+    const uint32_t* dyn = p.a.dyn_m;
     void* args[] = {&e, &splits, &M, &N, &dyn};
     const uint64_t wgs = std::min<uint64_t>(div_up((uint64_t)M * div_up(N, 4), 256), 8192);
     return hipLaunchKernel((const void*)&mm_join_kernel, dim3((uint32_t)wgs), dim3(256), args, 0,
                            stream);
+}
+
+template <int T, bool TA, bool TB>
+hipError_t launch_mm_sum(const MmInto& p, hipStream_t stream) {
+    const hipError_t st = launch_mm<T, TA, TB, MmSum>(p.a, p.sum(), p.plan, stream);
+    return st == hipSuccess ? launch_mm_join(p, stream) : st;
+}
+
+// Two products that do not need each other, p of a plain and a transposed operand, q of
+// two transposed ones: in one launch where they take tiles of one kind.
+template <int T>
+hipError_t launch_mm_two_sums(const MmInto& p, const MmInto& q, hipStream_t stream) {
+    hipError_t st;
+    if (p.plan.kind != q.plan.kind) {
+        st = launch_mm_sum<T, false, true>(p, stream);
+        return st == hipSuccess ? launch_mm_sum<T, true, true>(q, stream) : st;
+    }
+    const void* fn =
+        p.plan.kind == kTile256
+            ? (const void*)&mm_pair_kernel<MmShape256<T, false, true>, MmShape256<T, true, true>, MmSum>
+        : p.plan.kind == kTile128
+            ? (const void*)&mm_pair_kernel<MmShape128<T, false, true>, MmShape128<T, true, true>, MmSum>
+            : (const void*)&mm_pair_kernel<MmShapeSmall<T, false, true>, MmShapeSmall<T, true, true>, MmSum>;
+    MmArgs a1 = mm_planned(p.a, p.plan), a2 = mm_planned(q.a, q.plan);
+    MmSum::Args e1 = p.sum(), e2 = q.sum();
+    void* args[] = {&a1, &e1, &a2, &e2};
+    st = hipLaunchKernel(fn, dim3(a1.wgs * a1.splits + a2.wgs * a2.splits),
+                         dim3(tile_threads(p.plan.kind)), args, 0, stream);
+    if (st == hipSuccess)
+        st = launch_mm_join(p, stream);
+    return st == hipSuccess ? launch_mm_join(q, stream) : st;
 }
 
 }  // namespace zq
