@@ -300,6 +300,14 @@ def test_linear_grad_long_sums_split_and_equal_bits(shape):
         same(a, linear_grad(dy, codes, scales, 128, torch.float32, zq.ZQ_GRAD_WRITE))
 
 
+def test_linear_grad_of_the_most_tokens():
+    n, o, i = 1 << 20, 9, 16
+    dy = randn((n, o), 1, torch.bfloat16)
+    codes, scales, _ = quantized(randn((n, i), 2), 4096)
+    want, bound = linear_want(dy, codes, scales, 4096, None, torch.float32)
+    near(linear_grad(dy, codes, scales, 4096, torch.float32, zq.ZQ_GRAD_WRITE), want, bound)
+
+
 def test_linear_grad_infinities_stay_in_their_row():
     """The last token's step of 64 is ragged: what fills it up must not meet an
     infinity of dy or a NaN."""
@@ -375,6 +383,28 @@ def test_ce_loss(dtype, shape):
     for pad, id_type, scale, piece in ((0, torch.int64, 1.0, 0), (30, torch.int32, 0.5, 256), (30, torch.int64, -2.0, 700)):
         x, w, ids, there = ce_inputs(n, d, rows, dtype, n + d, pad, id_type)
         check_loss(ce_loss(x, w, ids, scale, piece), x, w, ids, there, scale)
+
+
+# Beyond 512 tokens the loss gathers those that count; from 1025 on the gathering takes 8 ids a thread, beyond 8192
+# more than one round; 2^20 tokens are the most.
+LONG = [(512, 64, 300), (513, 64, 300), (1024, 128, 65), (1025, 192, 777), (2050, 100, 515), (9000, 64, 130),
+        (1 << 20, 8, 5)]
+
+
+@pytest.mark.parametrize("pad", [0, 10, 60, 99])
+@pytest.mark.parametrize("shape", LONG)
+def test_ce_of_many_tokens(shape, pad):
+    n, d, rows = shape
+    x, w, ids, there = ce_inputs(n, d, rows, "bf16", n + pad, pad)
+    got = ce_loss(x, w, ids)
+    check_loss(got, x, w, ids, there, 1.0)
+    lse = torch.where(there, got[1], NAN)
+    dloss = torch.where(there, randn((n,), 9, std=30.0 / n), torch.full((n,), INF, device="cuda"))
+    dx, bx, dw, bw = ce_want(x, w, ids, there, 1.0, lse, dloss)
+    got = ce_grad(x, w, ids, 1.0, lse, dloss, torch.bfloat16)
+    assert not bool(got[0][~there].view(torch.int16).any())
+    near(got[0], dx, final(dx, bx, torch.bfloat16), "dx")
+    near(got[1], dw, final(dw, bw, torch.bfloat16), "dw")
 
 
 def test_ce_loss_of_tokens_that_are_all_left_out():
@@ -754,6 +784,41 @@ def test_a_captured_step_replays_to_the_eager_results():
             torch.cuda.synchronize()
             for x, y in zip(s.outputs(), w):
                 same(x, y)
+
+
+def test_two_graphs_may_share_a_workspace_in_turn():
+    n, d, rows = 600, 128, 900
+    ws = torch.empty(zq.ce_grad_workspace(n, rows, d, 256), dtype=torch.uint8, device="cuda")
+    graphs, outs, want = [], [], []
+    for k in range(2):
+        x, w, ids, there = ce_inputs(n, d, rows, "bf16", 10 * k, 20)
+        lse, dloss = exact_lse(x, w, ids, there, 1.0), randn((n,), k)
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+
+        def run():
+            zq.zq_ce_grad(x, w, ids, 1.0, lse, dloss, dx, dw, zq.ZQ_GRAD_WRITE, ws, piece=256)
+
+        run()
+        want.append((dx.clone(), dw.clone()))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            run()
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append((g, x, w, ids, lse, dloss))
+        outs.append((dx, dw))
+    for _ in range(3):
+        for (g, *_rest), out, w in zip(graphs, outs, want):
+            for o in out:
+                o.fill_(NAN)
+            g.replay()
+            ws.fill_(0xFF)                           # what lies there between calls means nothing
+            torch.cuda.synchronize()
+            for o, v in zip(out, w):
+                same(o, v)
 
 
 def test_calls_on_several_streams_at_once():
