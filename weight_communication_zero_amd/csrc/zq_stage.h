@@ -1,6 +1,7 @@
 // zq_stage.h -- operands of the matrix products laid out in a call's workspace:
 // rows of 16-bit values of the product's type with zeros up to a padded width, from
-// rows of any width or from qwZ codes, all rows or those of a list.
+// rows of any width or from qwZ codes, all rows or those of a list.  HBM's: 180 M codes
+// into bf16 take 91 us (5.9 TB/s), 67 M 16-bit values 42 us (6.4).
 #pragma once
 
 #include "zq_layers_launch.h"
