@@ -59,6 +59,14 @@ __device__ __forceinline__ i4v buffer_of(const void* p) {
     return r;
 }
 
+// The buffer `bytes` further on (scalar instructions, which need no distance).
+__device__ __forceinline__ i4v advanced(i4v r, uint64_t bytes) {
+    const uint64_t a = ((uint64_t)(uint32_t)r.y << 32 | (uint32_t)r.x) + bytes;
+    r.x = (int)(uint32_t)a;
+    r.y = (int)(uint32_t)(a >> 32);
+    return r;
+}
+
 // Waits until at most N of the wave's loads are under way.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -133,9 +141,8 @@ struct MmTile {
         dma16(srd, v, lds + (j * WAVES + wave) * 1024);
     }
 
-    __device__ __forceinline__ void load_all(const uint16_t* p, uint64_t ld, uint32_t left,
-                                             uint32_t lds, uint32_t wave) const {
-        const i4v srd = buffer_of(p);
+    __device__ __forceinline__ void load_all(i4v srd, uint64_t ld, uint32_t left, uint32_t lds,
+                                             uint32_t wave) const {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
             load(srd, j, ld, left, lds, wave);
@@ -271,9 +278,8 @@ __device__ __forceinline__ void mm_run(const MmArgs& a, const typename Epi::Args
     la.init(wave, lane, a.a.ld, S::TA ? a.a_cols - m0 : M - m0, listed ? a.a_rows + m0 : nullptr);
     lb.init(wave, lane, a.b.ld, S::TB ? a.b_cols - n0 : a.N - n0, nullptr);
     const uint64_t step_a = S::TA ? kMmK * a.a.ld : kMmK, step_b = S::TB ? kMmK * a.b.ld : kMmK;
-    const uint16_t* pa =
-        a.a.p + (S::TA ? (uint64_t)m0 : listed ? 0 : m0 * a.a.ld) + s0 * step_a;
-    const uint16_t* pb = a.b.p + (S::TB ? (uint64_t)n0 : n0 * a.b.ld) + s0 * step_b;
+    i4v pa = buffer_of(a.a.p + (S::TA ? (uint64_t)m0 : listed ? 0 : m0 * a.a.ld) + s0 * step_a);
+    i4v pb = buffer_of(a.b.p + (S::TB ? (uint64_t)n0 : n0 * a.b.ld) + s0 * step_b);
     const typename Epi::Row row = Epi::row(e, M, m0, tid);
 
     const uint32_t wm = wave / S::WN, wn = wave % S::WN;
@@ -327,8 +333,8 @@ __device__ __forceinline__ void mm_run(const MmArgs& a, const typename Epi::Args
             if (s < steps) {
                 la.load_all(pa, a.a.ld, count - s * kMmK, base_a + s * kA, wave);
                 lb.load_all(pb, a.b.ld, count - s * kMmK, base_b + s * kB, wave);
-                pa += step_a;
-                pb += step_b;
+                pa = advanced(pa, step_a * 2);
+                pb = advanced(pb, step_b * 2);
             }
         if (steps >= D)
             wait_vm<(D - 1) * (kLoadsA + kLoadsB)>();
@@ -348,14 +354,13 @@ __device__ __forceinline__ void mm_run(const MmArgs& a, const typename Epi::Args
         constexpr bool kMore = decltype(more)::value;  // step s + D is there to load
         const uint32_t left = count - (s + D) * kMmK;
         const uint32_t oa1 = oa == (D - 1) * kA ? 0 : oa + kA, ob1 = ob == D * kB ? 0 : ob + kB;
-        const i4v srd_a = buffer_of(pa), srd_b = buffer_of(pb);
         __builtin_amdgcn_sched_barrier(0);
         phase(MmInt<0>(), base_a + oa, base_b + ob, MmInt<1>(), [&](int i) {
             if constexpr (kMore)
 #pragma unroll
                 for (int j = 0; j < kLoadsB; ++j)
                     if (j * S::MI / kLoadsB == i)
-                        lb.load(srd_b, j, a.b.ld, left, base_b + ob_new, wave);
+                        lb.load(pb, j, a.b.ld, left, base_b + ob_new, wave);
         });
         // Past step s + 1's loads, those of steps s + 2 to s + D - 1 and the ones just
         // issued may be under way.
@@ -373,10 +378,10 @@ __device__ __forceinline__ void mm_run(const MmArgs& a, const typename Epi::Args
 #pragma unroll
                 for (int j = 0; j < kLoadsA; ++j)
                     if (j * S::MI / (2 * kLoadsA) == i)
-                        la.load(srd_a, j, a.a.ld, left, base_a + oa, wave);
+                        la.load(pa, j, a.a.ld, left, base_a + oa, wave);
         });
-        pa += step_a;
-        pb += step_b;
+        pa = advanced(pa, step_a * 2);
+        pb = advanced(pb, step_b * 2);
         oa = oa1;
         ob_new = ob;
         ob = ob1;

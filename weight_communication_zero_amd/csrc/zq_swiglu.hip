@@ -9,8 +9,8 @@
 // the plain int8 quantizer: a block is a group of adjacent lanes, or several parts
 // of the whole wave.  No LDS.
 //
-// Bound by HBM: 46 M elements in bf16, block 128, take 71 us forward (372 MB at 5.2
-// TB/s) and 59 us backward (6.3); 180 M elements backward with h 320 us (1.81 GB at
+// Bound by HBM: 46 M elements in bf16, block 128, take 70 us forward (372 MB at 5.3
+// TB/s) and 58 us backward (6.4); 180 M elements backward with h 315 us (1.81 GB at
 // 5.7).  A copy of the same card runs at 4.9.
 #include "zq_device.h"
 #include "zq_layers_launch.h"
@@ -21,26 +21,26 @@ namespace {
 
 // exp(x) for x <= 0, off by 1.5 ulp or so: the product with log2(e) is kept in two
 // parts, so that its rounding does not grow with |x| (4 instructions more than
-// exp2(x log2(e)), which at x = -80 is off by 40 ulp).
+// exp2(x log2(e)), which at x = -80 is off by 40 ulp).  Below -100 (and for NaN) that of
+// -100, which is 0 to within 2^-140: nothing is multiplied by an infinity.
 __device__ __forceinline__ float exp_neg(float x) {
     constexpr float kHi = 0x1.715476p0f, kLo = 0x1.4ae0cp-26f, kLn2 = 0x1.62e430p-1f;
+    x = __builtin_fmaxf(x, -100.0f);
     const float t = x * kHi;
-    float r = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
-    r = x > -88.0f ? r * kLn2 : 0.0f;  // below, exp2 gives 0 (and x may be infinite)
+    const float r = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
     const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e, r, e);
+    return __builtin_fmaf(e, r * kLn2, e);
 }
 
 // sigmoid(g) and 1 - sigmoid(g), neither by subtraction, so that both keep their
-// relative precision and nothing overflows.
+// relative precision and nothing overflows.  (Of a NaN they are 0 and 1: every use
+// multiplies by g itself.)
 __device__ __forceinline__ void sigmoid(float g, float* s, float* not_s) {
     const float a = exp_neg(-__builtin_fabsf(g));
     const float r = __builtin_amdgcn_rcpf(1.0f + a);
     const float q = a * r;
     *s = g >= 0.0f ? r : q;
     *not_s = g >= 0.0f ? q : r;
-    if (g != g)
-        *s = *not_s = g;
 }
 
 template <int B>
@@ -52,10 +52,25 @@ struct SwGeom {
     static constexpr int TILE = SUB * U;
 };
 
-// 8 elements from element e on; of the last ones, those at n and after are 0.
-template <int T, bool MASK>
-__device__ __forceinline__ void load8(const void* __restrict__ p, uint64_t e, uint64_t n,
-                                      float* x) {
+// The largest magnitude of 16-bit values, two a word, as binary32 bits: magnitudes
+// order like their bits (NaN above all), also after widening.
+template <int T>
+__device__ __forceinline__ uint32_t top_of(u4 w) {
+    typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+    us2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(us2, w[i] & 0x7FFF7FFFu));
+    const uint32_t top = max((uint32_t)m.x, (uint32_t)m.y);
+    return fbits(half_lo<T>(top));
+}
+
+// 8 elements from element e on; of the last ones, those at n and after are 0.  Gives
+// their largest magnitude's bits where TOP says so.
+template <int T, bool MASK, bool TOP = false>
+__device__ __forceinline__ uint32_t load8(const void* __restrict__ p, uint64_t e, uint64_t n,
+                                          float* x) {
+    uint32_t top = 0;
     if constexpr (!MASK) {
         if constexpr (T == kF32) {
             const f4 a = ld_stream((const f4*)((const float*)p + e));
@@ -68,6 +83,8 @@ __device__ __forceinline__ void load8(const void* __restrict__ p, uint64_t e, ui
             x[2] = half_lo<T>(w.y); x[3] = half_hi<T>(w.y);
             x[4] = half_lo<T>(w.z); x[5] = half_hi<T>(w.z);
             x[6] = half_lo<T>(w.w); x[7] = half_hi<T>(w.w);
+            if constexpr (TOP)
+                return top_of<T>(w);
         }
     } else {
 #pragma unroll
@@ -81,6 +98,12 @@ __device__ __forceinline__ void load8(const void* __restrict__ p, uint64_t e, ui
             }
         }
     }
+    if constexpr (TOP) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            top = max(top, absbits(x[j]));
+    }
+    return top;
 }
 
 template <int T, bool MASK>
@@ -110,44 +133,47 @@ __device__ __forceinline__ void store8(const float* x, void* __restrict__ p, uin
     }
 }
 
-// The kept form of a tile: scales, then codes.
+// The kept form of a tile, of which this lane's largest magnitude is `top`: scales, then
+// codes.  Adding 1.5 2^23 to a quotient rounds it to the nearest integer, ties to even,
+// and leaves its two's complement in the low bits: the codes' bytes are picked from
+// there.
 template <int B, bool MASK>
-__device__ __forceinline__ void keep(const float (&x)[SwGeom<B>::U][8], uint64_t base, int lane,
-                                     uint64_t n, int8_t* __restrict__ codes,
-                                     float* __restrict__ scales) {
+__device__ __forceinline__ void keep(const float (&x)[SwGeom<B>::U][8], uint32_t top,
+                                     uint64_t base, int lane, uint64_t n,
+                                     int8_t* __restrict__ codes, float* __restrict__ scales) {
     using G = SwGeom<B>;
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < G::U; ++u)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            m = max(m, absbits(x[u][j]));
-    const BlockScale s = block_scale<127>(group_max<G::LPB>(m));
+    constexpr float kInt = 0x1.8p23f;
+    const BlockScale s = block_scale<127>(group_max<G::LPB>(top));
     const uint64_t first = base + (uint64_t)lane * 8;
     if (lane % G::LPB == 0 && (!MASK || first < n))
         scales[first / B] = s.s;
 
     bool redo = false;
-    float k[G::U][8];
+    float f[G::U][8];
 #pragma unroll
     for (int u = 0; u < G::U; ++u)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            k[u][j] = code_fast<127>(x[u][j], s, redo);
-    if (redo) {
+        for (int j = 0; j < 8; ++j) {
+            const float y = x[u][j] * s.inv;
+            f[u][j] = y + kInt;
+            redo |= __builtin_fabsf(y - (f[u][j] - kInt)) > tie_band<127>();
+        }
+    if (redo | s.exact) {
 #pragma unroll
         for (int u = 0; u < G::U; ++u)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                k[u][j] = code_fix<127>(x[u][j], s, k[u][j]);
+                f[u][j] = code_fix<127>(x[u][j], s, f[u][j] - kInt) + kInt;
     }
 #pragma unroll
     for (int u = 0; u < G::U; ++u) {
         const uint64_t e = base + (uint64_t)u * G::SUB + (uint64_t)lane * 8;
-        u2 v = {0, 0};
+        u2 v;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j / 4] |= ((uint32_t)code_clamp<127>(k[u][j]) & 0xFFu) << (8 * (j & 3));
+        for (int h = 0; h < 2; ++h)
+            v[h] = __builtin_amdgcn_perm(fbits(f[u][4 * h + 1]), fbits(f[u][4 * h]), 0x0C0C0400u) |
+                   __builtin_amdgcn_perm(fbits(f[u][4 * h + 3]), fbits(f[u][4 * h + 2]),
+                                         0x04000C0Cu);
         if constexpr (!MASK) {
             st_stream(v, (u2*)(codes + e));
         } else {
@@ -165,12 +191,13 @@ __device__ __forceinline__ void forward_tile(const SwigluArgs& a, uint64_t tile)
     const int lane = lane_id();
     const uint64_t base = tile * G::TILE;
     float g[G::U][8], v[G::U][8];
+    uint32_t g_top = 0, v_top = 0;
 #pragma unroll
-    for (int u = 0; u < G::U; ++u)
-        load8<T, MASK>(a.gate, base + (uint64_t)u * G::SUB + (uint64_t)lane * 8, a.n, g[u]);
-#pragma unroll
-    for (int u = 0; u < G::U; ++u)
-        load8<T, MASK>(a.up, base + (uint64_t)u * G::SUB + (uint64_t)lane * 8, a.n, v[u]);
+    for (int u = 0; u < G::U; ++u) {
+        const uint64_t e = base + (uint64_t)u * G::SUB + (uint64_t)lane * 8;
+        g_top = max(g_top, load8<T, MASK, true>(a.gate, e, a.n, g[u]));
+        v_top = max(v_top, load8<T, MASK, true>(a.up, e, a.n, v[u]));
+    }
 #pragma unroll
     for (int u = 0; u < G::U; ++u) {
         float h[8];
@@ -182,8 +209,8 @@ __device__ __forceinline__ void forward_tile(const SwigluArgs& a, uint64_t tile)
         }
         store8<T, MASK>(h, a.h, base + (uint64_t)u * G::SUB + (uint64_t)lane * 8, a.n);
     }
-    keep<B, MASK>(g, base, lane, a.n, a.gate_codes, a.gate_scales);
-    keep<B, MASK>(v, base, lane, a.n, a.up_codes, a.up_scales);
+    keep<B, MASK>(g, g_top, base, lane, a.n, a.gate_codes, a.gate_scales);
+    keep<B, MASK>(v, v_top, base, lane, a.n, a.up_codes, a.up_scales);
 }
 
 template <int T, int B>
