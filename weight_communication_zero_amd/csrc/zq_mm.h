@@ -74,6 +74,13 @@ __device__ __forceinline__ void wait_vm() {
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// All waves' arrival; no access to memory moves across it.
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <int T>
 __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
     if constexpr (T == kBF16) {
@@ -87,11 +94,6 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
     }
 }
 
-// The LDS side of one operand of ROWS rows.  Stored by 16-byte chunks so that
-// the reads below meet no bank twice (transposed tiles of fewer than 128 rows apart):
-//   plain       row r, chunk c of 8 at (r, c ^ (r & 7))
-//   transposed  k, pair of chunks q at (k, q ^ mm_turn(k))
-
 // The turn of a transposed tile's row of ROWS / 16 pairs: the 16 k's of one read are
 // 8 q + 0 .. 3 for q = 0 .. 3.
 template <int ROWS>
@@ -99,6 +101,10 @@ __device__ __forceinline__ uint32_t mm_turn(uint32_t k) {
     return ((k & 3) + 4 * ((k >> 3) & 1)) & (ROWS >= 128 ? 7 : ROWS / 16 - 1);
 }
 
+// The LDS side of one operand of ROWS rows.  Stored by 16-byte chunks so that
+// the reads below meet no bank twice (transposed tiles of fewer than 128 rows apart):
+//   plain       row r, chunk c of 8 at (r, c ^ (r & 7))
+//   transposed  k, pair of chunks q at (k, q ^ mm_turn(k))
 template <int ROWS, bool TR, int WAVES>
 struct MmTile {
     static constexpr uint32_t kBytes = ROWS * kMmK * 2;
@@ -340,7 +346,7 @@ __device__ __forceinline__ void mm_run(const MmArgs& a, const typename Epi::Args
             wait_vm<(D - 1) * (kLoadsA + kLoadsB)>();
         else
             wait_vm<0>();
-        __builtin_amdgcn_s_barrier();
+        meet();
         clear(0, 0, 0);
 #pragma unroll
         for (int i = 0; i < S::MI; ++i)
@@ -369,7 +375,7 @@ __device__ __forceinline__ void mm_run(const MmArgs& a, const typename Epi::Args
             wait_vm<(D - 2) * (kLoadsA + kLoadsB) + kLoadsB>();
         else
             wait_vm<0>();
-        __builtin_amdgcn_s_barrier();
+        meet();
         if constexpr (!kMore)
             clear(s + 1, oa1, ob1);
         __builtin_amdgcn_sched_barrier(0);
@@ -392,7 +398,7 @@ __device__ __forceinline__ void mm_run(const MmArgs& a, const typename Epi::Args
     for (; s < steps; ++s)
         step(s, MmInt<0>());
     wait_lds();
-    __builtin_amdgcn_s_barrier();
+    meet();
     // acc[i][j][r] is C at m = m0 + wm BM / WM + 16 i + (lane & 15),
     // n = n0 + wn BN / WN + 16 j + 4 (lane >> 4) + r.
     Epi::template finish<S>(e, row, acc, M, a.N, m0, n0, split, wm, wn, lane, lds);
