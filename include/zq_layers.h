@@ -40,7 +40,8 @@ extern "C" {
  *   gate_codes, gate_scales = zq_quant_int8(gate);  up_codes, up_scales likewise
  * in one pass over the inputs.  Codes and scales equal zq_quant_int8's bit for
  * bit.  h is formed in binary32 from the inputs themselves (not from the kept
- * values), off by at most 2^-21 times itself before its rounding.
+ * values), off by at most 2^-21 times itself before its rounding (a sigmoid below
+ * 2^-126 counts as 0).
  *
  *   gate, up   [n] fp32, bf16 or fp16 (dtype), read only; they may be one buffer.
  *   h          [n] of dtype, written.
@@ -112,8 +113,9 @@ size_t zq_linear_grad_workspace(size_t n_tok, uint64_t out_dim, uint64_t in_dim)
  *   ids    [n_tok] int32 or int64 (id_type), aligned to their size, read only.
  *   loss   [n_tok] fp32, written.
  *   lse    [n_tok] fp32, written: what zq_ce_grad needs.
- *   piece  rows of w worked on at a time, or 0 for the library's choice: a larger
- *          piece takes a larger workspace and fewer launches.
+ *   piece  rows of w worked on at a time (rounded up to a multiple of 256), or 0 for
+ *          the library's choice: a larger piece takes a larger workspace and fewer
+ *          launches.
  *   workspace  at least zq_ce_loss_workspace(n_tok, rows, dim, piece) bytes.
  * The sum runs in binary32 over tiles of the vocabulary, each with a maximum of
  * its own taken out; nothing of size n_tok * rows is stored.
