@@ -584,11 +584,20 @@ def _current(t) -> int:
     return dev if dev >= 0 and dev == _device() else -2
 
 
+def _stream_on(stream, device: int) -> int | None:
+    """_stream, where a tensor on the current device says that there is one."""
+    return _stream(stream) if stream is not None or _raw_stream is None else _raw_stream(device)
+
+
+_swiglu, _swiglu_grad = lib.zq_swiglu_int8, lib.zq_swiglu_grad_int8
+
+
 def zq_swiglu_int8(gate, up, block: int, h, gate_codes, gate_scales, up_codes, up_scales,
                    stream=None) -> None:
     """h = gate * sigmoid(gate) * up (fp32/bf16/fp16, all of one dtype), and gate
     and up as zq_quant_int8 blocks for zq_swiglu_grad_int8."""
-    n, dt, dev, nb = gate.numel(), gate.dtype, _current(gate), _blocks(gate.numel(), block)
+    n, dt, dev = gate.numel(), gate.dtype, _current(gate)
+    nb = _blocks(n, block)
     ptr = torch.Tensor.data_ptr
     if not (_fits(gate, dt, n, dev) and _fits(up, dt, n, dev) and _fits(h, dt, n, dev)
             and _fits(gate_codes, torch.int8, n, dev) and _fits(up_codes, torch.int8, n, dev)
@@ -600,10 +609,11 @@ def zq_swiglu_int8(gate, up, block: int, h, gate_codes, gate_scales, up_codes, u
                                    ("up_codes", up_codes, n, _I8),
                                    ("up_scales", up_scales, nb, _F32)):
             _need(name, t, m, dtypes)
-        ptr = _p
-    _check("zq_swiglu_int8",
-           lib.zq_swiglu_int8(ptr(gate), ptr(up), _dtype(gate), n, block, ptr(h), ptr(gate_codes),
-                              ptr(gate_scales), ptr(up_codes), ptr(up_scales), _stream(stream)))
+        ptr, dev = _p, _device()
+    st = _swiglu(ptr(gate), ptr(up), _dtype(gate), n, block, ptr(h), ptr(gate_codes),
+                 ptr(gate_scales), ptr(up_codes), ptr(up_scales), _stream_on(stream, dev))
+    if st:
+        _check("zq_swiglu_int8", st)
 
 
 def zq_swiglu_grad_int8(gate_codes, gate_scales, up_codes, up_scales, block: int, dh, dgate, dup,
@@ -611,7 +621,8 @@ def zq_swiglu_grad_int8(gate_codes, gate_scales, up_codes, up_scales, block: int
     """dgate and dup of zq_swiglu_int8 at its kept values, for h's gradient dh
     (fp32/bf16/fp16, all of one dtype); h, where given, gets the product of the
     kept values."""
-    n, dt, dev, nb = dh.numel(), dh.dtype, _current(dh), _blocks(dh.numel(), block)
+    n, dt, dev = dh.numel(), dh.dtype, _current(dh)
+    nb = _blocks(n, block)
     ptr = torch.Tensor.data_ptr
     if not (_fits(dh, dt, n, dev) and _fits(dgate, dt, n, dev) and _fits(dup, dt, n, dev)
             and (h is None or _fits(h, dt, n, dev)) and _fits(gate_codes, torch.int8, n, dev)
@@ -624,11 +635,12 @@ def zq_swiglu_grad_int8(gate_codes, gate_scales, up_codes, up_scales, block: int
                                    ("dgate", dgate, n, (dt,)), ("dup", dup, n, (dt,)),
                                    ("h", h, n, (dt,))):
             _need(name, t, m, dtypes)
-        ptr = _p
-    _check("zq_swiglu_grad_int8",
-           lib.zq_swiglu_grad_int8(ptr(gate_codes), ptr(gate_scales), ptr(up_codes),
-                                   ptr(up_scales), block, ptr(dh), _dtype(dh), n, ptr(dgate),
-                                   ptr(dup), None if h is None else ptr(h), _stream(stream)))
+        ptr, dev = _p, _device()
+    st = _swiglu_grad(ptr(gate_codes), ptr(gate_scales), ptr(up_codes), ptr(up_scales), block,
+                      ptr(dh), _dtype(dh), n, ptr(dgate), ptr(dup), None if h is None else ptr(h),
+                      _stream_on(stream, dev))
+    if st:
+        _check("zq_swiglu_grad_int8", st)
 
 
 def linear_grad_workspace(n_tok: int, out_dim: int, in_dim: int) -> int:
