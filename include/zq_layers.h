@@ -156,8 +156,9 @@ size_t zq_ce_loss_workspace(size_t n_tok, uint64_t rows, uint64_t dim, uint64_t 
  * dloss are not used.  The logits are formed again, a piece of the vocabulary at
  * a time, and q is rounded to dtype before the two products (the matrix units
  * take 16-bit operands): an error of at most half a step of dtype per q, of the
- * size that the rounding of dx to dtype has.  It is the same for an fp32 dw,
- * whose 32 bits are for adding many micro-batches.  In fp16, q is scaled by the
+ * size that the rounding of dx to dtype has (with 128 tokens or fewer q is kept in
+ * two 16-bit parts, and the error is 2^-8 of that in bf16, 2^-11 in fp16).  It is
+ * the same for an fp32 dw, whose 32 bits are for adding many micro-batches.  In fp16, q is scaled by the
  * power of two that brings the largest finite |dloss| to [2^14, 2^15) and back
  * afterwards: a q below 2^-39 times that maximum vanishes.
  *

@@ -478,9 +478,10 @@ def ce_grad(x, w, ids, scale, lse, dloss, dw, mode=zq.ZQ_GRAD_WRITE, piece=0, co
     return dx.check() if dx else None, out.check() if out else None
 
 
-def ce_want(x, w, ids, there, scale, lse, dloss):
-    """dx and dw in 64 bits, and what the roundings before the output's may do."""
-    u, t = U[x.dtype], x.dtype
+def ce_want(x, w, ids, there, scale, lse, dloss, u=None):
+    """dx and dw in 64 bits, and what the roundings before the output's may do; u:
+    q's relative rounding."""
+    u, t = U[x.dtype] if u is None else u, x.dtype
     xs, ws, y = x[there].double(), w.double(), ids[there].long()
     z, off = logits(x[there], w, scale)
     g, l = dloss[there].double()[:, None], lse[there].double()[:, None]
@@ -533,6 +534,21 @@ def test_ce_grad(dtype, shape):
         old = randn((rows, d), 12, t)
         near(ce_grad(x, w, ids, scale, lse, dloss, old, zq.ZQ_GRAD_ADD, piece)[1], dw + old.double(),
              final(dw + old.double(), bw + 2.0 ** -23 * old.double().abs(), t), "dw added 16-bit")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n", [1, 31, 64, 128])
+def test_ce_grad_of_few_tokens_keeps_q_in_two_parts(n, dtype):
+    """q's rounding is off by half a step of half a step; an fp32 dw shows it.  (A second
+    part is below 2^-8 or 2^-11 of q and rounded by as much again.)"""
+    x, w, ids, there = ce_inputs(n, 200, 1500, dtype, n, 20)
+    lse = exact_lse(x, w, ids, there, 1.0)
+    dloss = torch.where(there, randn((n,), 9), torch.full((n,), NAN, device="cuda"))
+    dx, bx, dw, bw = ce_want(x, w, ids, there, 1.0, lse, dloss, u=U[T[dtype]] ** 2)
+    for piece in (0, 512):
+        got = ce_grad(x, w, ids, 1.0, lse, dloss, torch.float32, piece=piece)
+        near(got[1], dw, final(dw, bw, torch.float32), "dw")
+        near(got[0], dx, final(dx, bx, T[dtype]), "dx")
 
 
 def test_ce_grad_of_tokens_that_are_all_left_out():

@@ -10,6 +10,7 @@ namespace zq {
 // Scalars in the workspace.
 struct CeScalars {
     uint32_t count;    // tokens that count
+    uint32_t twice;    // two times that
     float up, down;    // the power of two that scales q, and its inverse
 };
 
@@ -100,6 +101,7 @@ __global__ __launch_bounds__(1024) void ce_prep_kernel(CePrepArgs a) {
     }
     if (threadIdx.x == 0) {
         a.t.scalars->count = count;
+        a.t.scalars->twice = 2 * count;
         if constexpr (GRAD) {
             for (int w = 0; w < 16; ++w)
                 top = max(top, maxima[w]);
@@ -118,6 +120,7 @@ __global__ __launch_bounds__(1024) void ce_prep_kernel(CePrepArgs a) {
 struct CeLayout {
     uint64_t kp;              // width of staged rows: dim up to a multiple of 64
     uint32_t piece, n_pieces;
+    uint32_t parts;           // of q: 1 or 2 (gradient)
     MmPlan logits;
     uint64_t scalars, list, target, lse, dloss, x, w;
     uint64_t part, run, z_target;   // loss
@@ -154,7 +157,7 @@ inline void ce_take_tokens(CeLayout& l, CeTake& take, uint32_t n_tok, bool grad)
     l.target = take((uint64_t)n_tok * 4);
     l.lse = take(grad ? (uint64_t)n_tok * 4 : 0);
     l.dloss = take(grad ? (uint64_t)n_tok * 4 : 0);
-    l.x = take(n_tok * l.kp * 2);
+    l.x = take(n_tok * l.kp * 2 * l.parts);
     l.w = take(l.piece * l.kp * 2);
 }
 
@@ -183,6 +186,7 @@ inline StageArgs ce_stage_x(const CeArgs& a, const CeLayout& l, const CeTokens& 
     s.list = t.list;
     s.count = &t.scalars->count;
     s.clear = (uint16_t*)a.dx;
+    s.twice = l.parts - 1;
     return s;
 }
 

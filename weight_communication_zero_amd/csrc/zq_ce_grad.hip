@@ -15,11 +15,26 @@
 namespace zq {
 namespace {
 
+// Up to this many tokens q is kept in two 16-bit parts (rows 2 t and 2 t + 1, which dx's
+// product adds up in pairs and dw's sums over, x's rows standing twice), so that its
+// rounding is off by 2^-16 (bf16) or 2^-22 (fp16) of it.  With few tokens one rounding
+// weighs more, as nothing averages out, and the products wait for memory and launches:
+// 64 tokens, 2048 x 32000 in bf16, take 175 us in two parts and 169 in one, 128 tokens
+// 205 and 178, 256 tokens 261 and 211.
+constexpr uint32_t kTwoParts = 128;
+
+// What a first part leaves of q: nothing where it is infinite or NaN.
+__device__ __forceinline__ float rest(float q, float first) {
+    const float r = q - first;
+    return __builtin_fabsf(r) < __builtin_inff() ? r : 0.0f;
+}
+
 struct Residual {
     struct Args {
         float scale;
         uint16_t* q;
         uint64_t ldq;
+        uint32_t parts;
         CeTokens t;
         uint32_t v0;
     };
@@ -50,7 +65,7 @@ struct Residual {
         const float factor = base2(e.scale);
         const uint32_t end = (N + kMmK - 1) / kMmK * kMmK;  // zeros from N up to here
         mm_rows<S>(
-            acc, wm, wn, lane, lds, [](uint32_t, uint32_t) { return f4{0, 0, 0, 0}; },
+            acc, wm, wn, lane, lds, false, [](uint32_t, uint32_t) { return f4{0, 0, 0, 0}; },
             [&](uint32_t r, uint32_t c, f4 z, f4) {
                 const uint32_t m = m0 + r, n = n0 + c;
                 if (m >= M || n >= end)
@@ -63,8 +78,15 @@ struct Residual {
                     q[k] = t.g * (n + k == t.target ? p - 1.0f : p);
                     q[k] = n + k < N ? q[k] : 0.0f;
                 }
-                *(u2*)(e.q + m * e.ldq + n) =
-                    u2{pack_half_rne<S::T>(q[0], q[1]), pack_half_rne<S::T>(q[2], q[3])};
+                const u2 first = {pack_half_rne<S::T>(q[0], q[1]), pack_half_rne<S::T>(q[2], q[3])};
+                uint16_t* out = e.q + (uint64_t)m * e.parts * e.ldq + n;
+                *(u2*)out = first;
+                if (e.parts == 2)
+                    *(u2*)(out + e.ldq) =
+                        u2{pack_half_rne<S::T>(rest(q[0], half_lo<S::T>(first.x)),
+                                               rest(q[1], half_hi<S::T>(first.x))),
+                           pack_half_rne<S::T>(rest(q[2], half_lo<S::T>(first.y)),
+                                               rest(q[3], half_hi<S::T>(first.y)))};
             });
     }
 };
@@ -72,6 +94,7 @@ struct Residual {
 CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
     CeLayout l = {};
     l.kp = round_up(dim, kMmK);
+    l.parts = n_tok <= kTwoParts ? 2 : 1;
     const uint64_t n_pad = round_up(n_tok, 256);
     // The library's choice: 512 MiB of q and of staged rows.
     uint64_t most = piece ? round_up(std::min<uint64_t>(piece, rows), 256)
@@ -81,13 +104,14 @@ CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
     l.logits = mm_plan(n_tok, l.piece, l.kp, false);
     CeTake take;
     ce_take_tokens(l, take, n_tok, true);
-    l.q = take((uint64_t)n_tok * l.piece * 2);
+    l.q = take((uint64_t)n_tok * l.piece * 2 * l.parts);
     l.ldacc = round_up(dim, 4);
     l.acc = take(l.n_pieces > 1 ? n_tok * l.ldacc * 4 : 0);
     uint64_t x_floats = 0, w_floats = 0;
     for (uint32_t n : {l.piece, l.rows_of(l.n_pieces - 1, rows)}) {
-        x_floats = std::max(x_floats, part_floats(mm_plan(n_tok, dim, n, true), n_tok, dim));
-        w_floats = std::max(w_floats, part_floats(mm_plan(n, dim, n_tok, true), n, dim));
+        const uint32_t k = n_tok * l.parts;
+        x_floats = std::max(x_floats, part_floats(mm_plan(k, dim, n, true), k, dim));
+        w_floats = std::max(w_floats, part_floats(mm_plan(n, dim, k, true), n, dim));
     }
     l.x_sums = take(x_floats * 4);
     l.w_sums = take(w_floats * 4);
@@ -112,13 +136,13 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
             break;
         const MmOperand w = ce_piece(a, w_type, l, v0, ws);
         MmArgs m = {};
-        m.a = x;
+        m.a = {x.p, x.ld * l.parts};  // each row's first copy
         m.b = w;
         m.M = a.n_tok;
         m.N = n;
         m.K = (uint32_t)l.kp;
         m.dyn_m = count;
-        Residual::Args e = {a.scale, (uint16_t*)(ws + l.q), l.piece, tok, v0};
+        Residual::Args e = {a.scale, (uint16_t*)(ws + l.q), l.piece, l.parts, tok, v0};
         st = launch_mm<T, false, false, Residual>(m, e, l.logits, stream);
         if (st != hipSuccess)
             break;
@@ -127,8 +151,12 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
         o.ldo = a.dim;
         o.factor = &tok.scalars->down;
         o.scale = a.scale;
-        MmInto to_x = {m, o, mm_plan(a.n_tok, a.dim, n, true), (float*)(ws + l.x_sums)};
+        const uint32_t q_rows = a.n_tok * l.parts;
+        const uint32_t* q_count = l.parts == 2 ? &tok.scalars->twice : count;
+        MmInto to_x = {m, o, mm_plan(q_rows, a.dim, n, true), (float*)(ws + l.x_sums), l.parts == 2};
         to_x.a.a = q;
+        to_x.a.M = q_rows;
+        to_x.a.dyn_m = q_count;
         to_x.a.N = a.dim;
         to_x.a.K = n;
         to_x.a.b_cols = (uint32_t)l.kp;
@@ -137,15 +165,15 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
         to_x.o.out = a.dx;
         to_x.o.list = tok.list;
         to_x.o.type = T;
-        MmInto to_w = {{}, o, mm_plan(n, a.dim, a.n_tok, true), (float*)(ws + l.w_sums)};
+        MmInto to_w = {{}, o, mm_plan(n, a.dim, q_rows, true), (float*)(ws + l.w_sums)};
         to_w.a.a = q;
         to_w.a.b = x;
         to_w.a.M = n;
         to_w.a.N = a.dim;
-        to_w.a.K = a.n_tok;
+        to_w.a.K = q_rows;
         to_w.a.a_cols = l.piece;
         to_w.a.b_cols = (uint32_t)l.kp;
-        to_w.a.dyn_k = count;
+        to_w.a.dyn_k = q_count;
         to_w.o.out = (char*)a.dw + (uint64_t)v0 * a.dim * (dw_type == kF32 ? 4 : 2);
         to_w.o.type = dw_type;
         to_w.o.add = mode == kGradAdd;

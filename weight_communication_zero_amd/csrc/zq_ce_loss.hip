@@ -218,6 +218,7 @@ bool x_in_place(uint32_t n_tok, uint32_t dim) {
 CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
     CeLayout l = {};
     l.kp = round_up(dim, kMmK);
+    l.parts = 1;
     const uint64_t n_pad = round_up(n_tok, 256);
     // The library's choice: 256 MiB each of staged rows and of pairs.
     uint64_t most = piece ? round_up(std::min<uint64_t>(piece, rows), 256)

@@ -433,9 +433,11 @@ __global__ __launch_bounds__(S1::kThreads, 2) void mm_pair_kernel(MmArgs a1, typ
 // comes from memory).  Four at a time, so that their fetches are under way together.
 // Four rows of fragments in a part of LDS of the wave's own, chunk c of 16 bytes of a row
 // at c ^ (row & 15) (or a smaller mask), which meets no bank twice.
+// With `pairs`, rows 2 r and 2 r + 1 of the tile are added and handed over as row r.
 template <class S, class G, class F>
 __device__ __forceinline__ void mm_rows(f4 (&acc)[S::MI][S::NI], uint32_t wm, uint32_t wn,
-                                        uint32_t lane, unsigned char* lds, G&& fetch, F&& put) {
+                                        uint32_t lane, unsigned char* lds, bool pairs, G&& fetch,
+                                        F&& put) {
     constexpr int kGroup = S::kGroup;
     constexpr uint32_t kChunks = S::NI * 4;           // of 16 bytes in a row
     constexpr uint32_t kMask = kChunks < 16 ? kChunks - 1 : 15;
@@ -461,12 +463,15 @@ __device__ __forceinline__ void mm_rows(f4 (&acc)[S::MI][S::NI], uint32_t wm, ui
             for (int k = 0; k < kBatch; ++k) {
                 const uint32_t row = (c0 + k * 64) / kChunks, chunk = (c0 + k * 64) % kChunks;
                 v[k] = *(const f4*)(mine + (row * kChunks + (chunk ^ (row & kMask))) * 16);
-                old[k] = fetch(mw + g * kGroup * 16 + row, nw + chunk * 4);
+                if (pairs)  // (an odd row adds its own other half, and is not handed over)
+                    v[k] += *(const f4*)(mine + ((row ^ 1) * kChunks + (chunk ^ ((row ^ 1) & kMask))) * 16);
+                old[k] = fetch((mw + g * kGroup * 16 + row) >> pairs, nw + chunk * 4);
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const uint32_t row = (c0 + k * 64) / kChunks, chunk = (c0 + k * 64) % kChunks;
-                put(mw + g * kGroup * 16 + row, nw + chunk * 4, v[k], old[k]);
+                if (!pairs || row % 2 == 0)
+                    put((mw + g * kGroup * 16 + row) >> pairs, nw + chunk * 4, v[k], old[k]);
             }
         }
         wait_lds();
@@ -580,6 +585,7 @@ struct MmSum {
         MmOut o;
         float* part;
         uint64_t rows, ld;
+        bool pairs;  // rows 2 m and 2 m + 1 of the product are row m's two parts
     };
     using Row = MmNoRow;
     static __device__ __forceinline__ Row row(const Args&, uint32_t, uint32_t, uint32_t) {
@@ -592,8 +598,10 @@ struct MmSum {
                                                   uint32_t wm, uint32_t wn, uint32_t lane,
                                                   unsigned char* lds) {
         const bool part = e.part != nullptr;
+        m0 >>= e.pairs;
+        M >>= e.pairs;
         mm_rows<S>(
-            acc, wm, wn, lane, lds,
+            acc, wm, wn, lane, lds, e.pairs,
             [&](uint32_t r, uint32_t c) {
                 const uint32_t m = m0 + r, n = n0 + c;
                 return !part && m < M && n < N ? e.o.fetch(m, n, N - n) : f4{0, 0, 0, 0};
@@ -616,6 +624,7 @@ __global__ __launch_bounds__(256) static void mm_join_kernel(MmSum::Args e, uint
                                                              const uint32_t* dyn_m) {
     if (dyn_m)
         M = min(M, *dyn_m);
+    M >>= e.pairs;
     const uint32_t groups = (N + 3) / 4;
     const uint64_t total = (uint64_t)M * groups;
     for (uint64_t g = blockIdx.x * 256ull + threadIdx.x; g < total; g += gridDim.x * 256ull) {

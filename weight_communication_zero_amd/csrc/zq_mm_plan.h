@@ -105,9 +105,10 @@ struct MmInto {
     MmOut o;
     MmPlan plan;
     float* part;
+    bool pairs = false;  // MmSum's
 
     MmSum::Args sum() const {
-        return {o, plan.splits > 1 ? part : nullptr, a.M, round_up(a.N, 4)};
+        return {o, plan.splits > 1 ? part : nullptr, a.M, round_up(a.N, 4), pairs};
     }
 };
 

@@ -20,6 +20,7 @@ struct StageArgs {
     const uint32_t* count;
     uint16_t* clear;        // where set, rows list[r] of `dim` elements, r from *count on,
                             // are cleared in it
+    uint32_t twice;         // 1: every row stands twice, one behind the other
 };
 
 // A lane per group of 8 elements of the result; the calling workgroup is wg of wgs.
@@ -27,13 +28,13 @@ template <int T, int IN, bool WHOLE>
 __device__ __forceinline__ void stage_rows(const StageArgs& a, uint32_t wg, uint32_t wgs) {
     const uint32_t rows = a.count ? min(a.rows, *a.count) : a.rows;
     const uint32_t per_row = a.ld / 8;
-    const uint64_t groups = (uint64_t)(a.clear ? a.rows : rows) * per_row;
+    const uint64_t groups = (uint64_t)((a.clear ? a.rows : rows) << a.twice) * per_row;
     for (uint64_t g = wg * 256ull + threadIdx.x; g < groups; g += wgs * 256ull) {
-        const uint32_t r = (uint32_t)(g / per_row);
-        const uint32_t c = (uint32_t)(g - (uint64_t)r * per_row) * 8;
+        const uint32_t r2 = (uint32_t)(g / per_row), r = r2 >> a.twice;
+        const uint32_t c = (uint32_t)(g - (uint64_t)r2 * per_row) * 8;
         Raw<T, 8> v = {{0, 0, 0, 0}};
         if (r >= rows) {
-            if (c < a.dim)
+            if (c < a.dim && (r << a.twice) == r2)
                 store_group<T, 8, WHOLE, false>(v, a.clear, a.list[r] * a.dim + c,
                                                 (uint32_t)(a.dim - c));
             continue;
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(256) void stage_kernel(StageArgs a) {
 }
 
 inline uint32_t stage_wgs(const StageArgs& a) {
-    const uint64_t wgs = ((uint64_t)a.rows * (a.ld / 8) + 255) / 256;
+    const uint64_t wgs = (((uint64_t)a.rows << a.twice) * (a.ld / 8) + 255) / 256;
     return (uint32_t)(wgs < 65536 ? wgs : 65536);
 }
 
