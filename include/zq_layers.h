@@ -113,6 +113,7 @@ size_t zq_linear_grad_workspace(size_t n_tok, uint64_t out_dim, uint64_t in_dim)
  *   ids    [n_tok] int32 or int64 (id_type), aligned to their size, read only.
  *   loss   [n_tok] fp32, written.
  *   lse    [n_tok] fp32, written: what zq_ce_grad needs.
+ *   scale  any number; 0 makes all logits equal (and NaN where a sum is not finite).
  *   piece  rows of w worked on at a time (rounded up to a multiple of 256), or 0 for
  *          the library's choice: a larger piece takes a larger workspace and fewer
  *          launches.

@@ -2,6 +2,8 @@
 // count, gathered; the plan of a call's workspace; pieces of the projection.
 #pragma once
 
+#include <cmath>
+
 #include "zq_mm_plan.h"
 #include "zq_stage.h"
 
@@ -231,6 +233,22 @@ hipError_t ce_stage(const CeArgs& a, int w_type, const CeLayout& l, uint32_t i, 
     if (w)
         return launch_stage<T>(sw, w_type == kQ8 ? kQ8 : T, stream);
     return x && i == 0 ? launch_stage<T>(sx, T, stream) : hipSuccess;
+}
+
+// A logit is unit * (pre * sum): pre is the scale's sign and power of two, so that the
+// inner product is exact (but for what leaves binary32's range), and unit, in [1, 2), is
+// never a factor that makes NaN of an infinity.  A scale of 0 and one that is not finite
+// stand in pre as they are.
+struct CeScale {
+    float pre, unit;
+};
+
+inline CeScale ce_scale(float scale) {
+    if (scale == 0.0f || !std::isfinite(scale))
+        return {scale, 1.0f};
+    int e;
+    const float unit = 2.0f * std::frexp(std::fabs(scale), &e);
+    return {std::copysign(std::ldexp(1.0f, e - 1), scale), unit};
 }
 
 // Exponentials are taken in base 2: logits times log2(e) are one product of a sum with

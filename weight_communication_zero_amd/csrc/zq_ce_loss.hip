@@ -30,7 +30,7 @@ __device__ __forceinline__ float rebased(f2 p, float ref) {
 
 struct Stats {
     struct Args {
-        float scale;
+        CeScale scale;
         f2* part;          // [tile of the piece][ld]
         uint64_t ld;
         uint32_t v0;       // the piece's first row
@@ -68,17 +68,16 @@ struct Stats {
         __syncthreads();
         const uint32_t nw = n0 + wn * (S::BN / S::WN) + (lane >> 4) * 4;
         const bool whole = n0 + S::BN <= N;
-        const float sign = e.scale < 0.0f ? -1.0f : 1.0f, factor = base2(e.scale) * sign;
+        const float factor = base2(e.scale.unit);
 #pragma unroll
         for (int i = 0; i < S::MI; ++i) {
             const uint32_t r = wm * (S::BM / S::WM) + i * 16 + (lane & 15), m = m0 + r;
-            // The largest logit is the largest sum, or with a negative scale the smallest.
             float top = -__builtin_inff();
 #pragma unroll
             for (int j = 0; j < S::NI; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    acc[i][j][k] *= sign;
+                    acc[i][j][k] *= e.scale.pre;
                     if (!whole)
                         acc[i][j][k] =
                             nw + j * 16 + k < N ? acc[i][j][k] : -__builtin_inff();
@@ -259,7 +258,7 @@ hipError_t launch(const CeArgs& a, int w_type, hipStream_t stream) {
         m.N = n;
         m.K = (uint32_t)l.kp;
         m.dyn_m = count;
-        Stats::Args e = {a.scale,
+        Stats::Args e = {ce_scale(a.scale),
                          (f2*)(ws + l.part),
                          round_up(a.n_tok, 256),
                          v0,
