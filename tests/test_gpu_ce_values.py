@@ -108,3 +108,19 @@ def test_far_scales(scale):
     want = torch.logsumexp(z, 1)
     near(lse, want, bound, "lse")
     near(loss, want - z.gather(1, ids[:, None])[:, 0], 2 * bound, "loss")
+
+
+@pytest.mark.parametrize("scale", [1.0, -2.0, 0.3])
+@pytest.mark.parametrize("size", [1e10, 1e20, 1e37])
+@pytest.mark.parametrize("n,rows", [(5, 257), (300, 999), (700, 5000)])
+def test_huge_finite_logits(n, rows, size, scale):
+    """Half a unit in the last place of such a logit is an exponent of its own; sums go up to some 10^38."""
+    x, w = randn((n, 64), 1, torch.bfloat16, 0.1 * size ** 0.5), randn((rows, 64), 2, torch.bfloat16, size ** 0.5)
+    ids = some_ids(n, rows, 3)
+    z = x.double() @ w.double().t() * float(torch.tensor(scale))
+    off = (64 + 16) * 2.0 ** -24 * abs(scale) * (x.double().abs() @ w.double().abs().t()).max(1).values
+    want = torch.logsumexp(z, 1)
+    for piece in (0, 512):
+        loss, lse = ce_loss(x, w, ids, scale, piece)
+        near(lse, want, off + 2.0 ** -23 * (64 + want.abs()), "lse")
+        near(loss, want - z.gather(1, ids[:, None])[:, 0], 2 * off + 2.0 ** -22 * (64 + want.abs()), "loss")

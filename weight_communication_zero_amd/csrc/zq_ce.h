@@ -251,9 +251,8 @@ inline CeScale ce_scale(float scale) {
     return {std::copysign(std::ldexp(1.0f, e - 1), scale), unit};
 }
 
-// Exponentials are taken in base 2: logits times log2(e) are one product of a sum with
-// this factor (rounded once, so that it is off by 2^-24 of each logit).
-__device__ __forceinline__ float base2(float scale) { return scale * 0x1.715476p0f; }
+// Exponentials are taken in base 2: a factor or an exponent times log2(e), rounded once.
+__device__ __forceinline__ float base2(float x) { return x * 0x1.715476p0f; }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 

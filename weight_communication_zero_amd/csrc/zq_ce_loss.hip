@@ -1,10 +1,10 @@
 // zq_ce_loss.hip -- softmax cross entropy of the vocabulary projection.
 //
 // The logits of a tile of tokens x vocabulary stay in the matrix product's
-// registers: the epilogue takes each token's maximum m over the tile's columns, the
-// sum s of 2^(z - m), and the target's logit where it lies there, all of logits in
-// base 2 (times log2 e).  A second kernel joins the tiles' pairs,
-// (m, s) + (m', s') = (M, s 2^(m-M) + s' 2^(m'-M)).
+// registers: the epilogue takes each token's largest sum m over the tile's columns, the
+// sum s of 2^(f (a - m)), f = unit log2 e, and the target's sum where it lies there.  A
+// second kernel joins the tiles' pairs,
+// (m, s) + (m', s') = (M, s 2^(f (m - M)) + s' 2^(f (m' - M))).
 //
 // Bound by the matrix units with many tokens (16384 x 4096 x 32000 from int8 in 3.05 ms:
 // 1410 TFLOP/s, 0.07 ms of it the dequantization), by the read of w with few (one token,
@@ -22,10 +22,17 @@ __device__ __forceinline__ float reference(float m) {
     return __builtin_fabsf(m) < __builtin_inff() ? m : 0.0f;
 }
 
+// 2^(factor (a - ref)) of two sums.  The difference is taken before the factor: factor a
+// and factor ref, each rounded, would leave half a unit of the largest logit's last place
+// in the exponent, which is 1e-6 at logits of 14 and whole powers of two beyond 10^9.
+__device__ __forceinline__ float relative(float factor, float a, float ref) {
+    return exp2_of(factor * (a - ref));
+}
+
 // A pair's sum relative to another reference.  With an infinite maximum the sum is
 // 0, infinity or NaN, and stays so.
-__device__ __forceinline__ float rebased(f2 p, float ref) {
-    return __builtin_fabsf(p.x) < __builtin_inff() ? p.y * exp2_of(p.x - ref) : p.y;
+__device__ __forceinline__ float rebased(float factor, f2 p, float ref) {
+    return __builtin_fabsf(p.x) < __builtin_inff() ? p.y * relative(factor, p.x, ref) : p.y;
 }
 
 struct Stats {
@@ -84,7 +91,7 @@ struct Stats {
                     top = __builtin_fmaxf(top, acc[i][j][k]);
                 }
             top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-            top = factor * __builtin_fmaxf(top, __shfl_xor(top, 32));
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
             // Few waves hold a target of their 16 rows.
             const uint32_t target = m < M && targets[r] < N ? targets[r] : 0xFFFFFFFFu;
             const uint32_t off = target - nw;
@@ -97,7 +104,7 @@ struct Stats {
                     for (int k = 0; k < 4; ++k)
                         z = off == j * 16 + k ? acc[i][j][k] : z;
                 if (here)
-                    e.z_target[m] = factor * z;
+                    e.z_target[m] = z;
             }
             const float ref = reference(top);
             float sum = 0.0f;
@@ -105,7 +112,7 @@ struct Stats {
             for (int j = 0; j < S::NI; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    sum += exp2_of(__builtin_fmaf(factor, acc[i][j][k], -ref));
+                    sum += relative(factor, acc[i][j][k], ref);
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
             if (lane < 16)
@@ -121,7 +128,7 @@ struct Stats {
             float sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < S::WN; ++w)
-                sum += rebased(pair[w * S::BM + r], ref);
+                sum += rebased(factor, pair[w * S::BM + r], ref);
             if (m0 + r < M)
                 e.part[(uint64_t)(n0 / S::BN) * e.ld + m0 + r] = f2{top, sum};
         }
@@ -138,6 +145,7 @@ struct JoinArgs {
     const void* ids;               // their ids
     uint32_t id64;
     float *loss, *lse;
+    float unit;
 };
 
 // Joins a piece's tiles with what earlier pieces gave.  ROWS tokens a workgroup,
@@ -151,9 +159,10 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     const uint32_t m = blockIdx.x * ROWS + row;
     const uint32_t count = a.count ? *a.count : a.n_tok;
     f2 mine = {-__builtin_inff(), 0.0f};
-    auto add = [&mine](f2 p) {
+    const float factor = base2(a.unit);
+    auto add = [&mine, factor](f2 p) {
         const float top = __builtin_fmaxf(mine.x, p.x), ref = reference(top);
-        mine = f2{top, rebased(mine, ref) + rebased(p, ref)};
+        mine = f2{top, rebased(factor, mine, ref) + rebased(factor, p, ref)};
     };
     if (m < count) {
         uint32_t t = k;
@@ -185,7 +194,6 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
         a.run[m] = mine;
         return;
     }
-    constexpr float kLn2 = 0x1.62e430p-1f;
     const float ref = reference(mine.x), log_sum = logf(mine.y);
     uint32_t t = m;
     if (a.list) {
@@ -199,8 +207,8 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
             return;
         }
     }
-    a.lse[t] = __builtin_fmaf(ref, kLn2, log_sum);
-    a.loss[t] = __builtin_fmaf(ref - a.z_target[m], kLn2, log_sum);
+    a.lse[t] = __builtin_fmaf(a.unit, ref, log_sum);
+    a.loss[t] = __builtin_fmaf(a.unit, ref - a.z_target[m], log_sum);
 }
 
 // Up to this many tokens the loss is formed for all of them, also those that are left
@@ -271,7 +279,8 @@ hipError_t launch(const CeArgs& a, int w_type, hipStream_t stream) {
             break;
         JoinArgs j = {e.part, e.ld, (uint32_t)div_up(n, tile_cols(l.logits.kind)), i == 0,
                       i + 1 == l.n_pieces, a.n_tok, a.rows, (f2*)(ws + l.run), e.z_target,
-                      all ? nullptr : tok.list, count, a.ids, a.id64, a.loss, a.lse_out};
+                      all ? nullptr : tok.list, count, a.ids, a.id64, a.loss, a.lse_out,
+                      e.scale.unit};
         void* args[] = {&j};
         // Few tokens: more threads each, so that no thread walks a long line of tiles.
         const uint32_t rows = a.n_tok <= 512 ? 2 : 16;
