@@ -6,6 +6,7 @@ What the tolerances count (2^-24 is half a step of binary32 relative to the valu
           the worst order; the scale's product 2^-24 of the logit more
   lse     what the logits are off by, and 2^-23 (64 + V / 2048 + |lse|) for the
           exponentials and their sum
+  loss    relative, at the tests that count it
 """
 import math
 
@@ -124,3 +125,86 @@ def test_huge_finite_logits(n, rows, size, scale):
         loss, lse = ce_loss(x, w, ids, scale, piece)
         near(lse, want, off + 2.0 ** -23 * (64 + want.abs()), "lse")
         near(loss, want - z.gather(1, ids[:, None])[:, 0], 2 * off + 2.0 ** -22 * (64 + want.abs()), "loss")
+
+
+def exact_operands(n, d, rows, dtype, seed, sign):
+    """Whole numbers, so that every sum is exact: rows of w in -4 .. 4, hidden states that
+    lean to their token by 0, 1, 2 or 3 times its row (sign -1: away from it)."""
+    w = torch.randint(-4, 5, (rows, d), generator=gen(seed), device="cuda")
+    ids = some_ids(n, rows, seed + 1)
+    lean = torch.arange(n, device="cuda")[:, None] % 4 * sign
+    x = torch.randint(-2, 3, (n, d), generator=gen(seed + 2), device="cuda") + lean * w[ids]
+    return x.to(T[dtype]), w.to(T[dtype]), ids
+
+
+@pytest.mark.parametrize("dtype,scale", [("bf16", 2.0 ** -6), ("fp16", 0.02), ("bf16", -0.02)])
+@pytest.mark.parametrize("n,rows", [(1, 2), (7, 1000), (300, 999), (300, 50257), (700, 2), (700, 8191)])
+def test_losses_of_sure_tokens_keep_their_digits(n, rows, dtype, scale):
+    """loss = log1p(X), X the sum over j != t of exp(z_j - z_t), M the largest z but z_t.  An
+    exponent z_j - M or M - z_t in base 2 has a difference's rounding, the factor's two and
+    the product's, 2^-24 each, and the exponential itself 2^-23: X is off by those of its
+    terms and by 2^-23 (64 + V / 2048) of itself for the sum, the loss by that over 1 + X
+    and 2^-22 of itself for the last steps.  A term below 2^-126 may vanish."""
+    sure = 0
+    for seed in (10, 20):
+        x, w, ids = exact_operands(n, 128, rows, dtype, seed, 1 if scale > 0 else -1)
+        if n == 1:
+            x = (x + 3 * math.copysign(1, scale) * w[ids]).to(x.dtype)
+        z = x.double() @ w.double().t() * float(torch.tensor(scale))
+        t = z.gather(1, ids[:, None])
+        others = z.scatter(1, ids[:, None], -INF)
+        top = others.max(1, keepdim=True).values
+        e = torch.exp(others - t)
+        total = e.sum(1)
+        e = torch.where(e > 0, e * ((others - top).abs() + (top - t).abs() + 2), 0.0)
+        want = torch.log1p(total)
+        bound = 2.0 ** -22 * e.sum(1) + 2.0 ** -23 * (64 + rows / 2048) * total + rows * 2.0 ** -126
+        bound = bound / (1 + total) + 2.0 ** -22 * want
+        assert bool((bound < 2e-4 * want + 1e-30).all())
+        sure += int((want < 1e-3).sum())
+        for piece in (0, 512):
+            loss, lse = ce_loss(x, w, ids, scale, piece)
+            assert bool((loss >= 0).all())
+            near(loss, want, bound, "loss")
+            near(lse, torch.logsumexp(z, 1), bound + 2.0 ** -23 * (1 + z.abs().max(1).values), "lse")
+    assert sure > 0
+
+
+def test_a_token_that_has_the_vocabulary_to_itself():
+    x, w, ids = randn((9, 64), 1, torch.bfloat16), randn((1, 64), 2, torch.bfloat16), some_ids(9, 1, 3)
+    loss, lse = ce_loss(x, w, ids)
+    z = (x.double() @ w.double().t())[:, 0]
+    assert not bool(loss.view(torch.int32).any())
+    near(lse, z, 80 * 2.0 ** -24 * (x.double().abs() @ w.double().abs().t())[:, 0])
+
+
+@pytest.mark.parametrize("piece", [0, 256])
+def test_infinite_and_nan_logits_of_targets_and_others(piece):
+    """Each token has its own mixture: an infinity (of either sign) or NaN at its target,
+    at another row, at both, everywhere else."""
+    rows, n = 700, 12
+    w = torch.zeros(rows, 64, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(n, 64, dtype=torch.bfloat16, device="cuda")
+    z = torch.zeros(n, rows, dtype=torch.float64, device="cuda")
+    ids = torch.full((n,), 300, device="cuda")
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[300] = False
+    one = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    one[600] = True
+    plan = [(~rest, INF), (~rest, -INF), (~rest, NAN), (one, INF), (one, -INF), (one, NAN), (rest, -INF), (rest, INF),
+            (~rest | one, INF), (~rest | one, -INF), (rest | ~rest, -INF), (~rest, 0.0)]
+    for t, (where, value) in enumerate(plan):
+        # Token t reads column t of w alone: 0 but where its value stands.
+        x[t] = 0
+        w[where, t] = 2.0 ** 100 if value == INF else -2.0 ** 100 if value == -INF else value
+        z[t, where] = value
+    # 2^100 times 2^100 is infinite; NaN stands in w, where all tokens meet it: its token comes apart.
+    for t in range(n):
+        ww = torch.zeros_like(w)
+        ww[:, t] = w[:, t]
+        xx = torch.zeros_like(x)
+        xx[t, t] = 2.0 ** 100
+        loss, lse = ce_loss(xx, ww, ids, 1.0, piece)
+        want = torch.logsumexp(z[t], 0)
+        near(lse[t:t + 1], want[None], 2.0 ** -16, f"lse {t}")
+        near(loss[t:t + 1], (want - z[t, 300])[None], 2.0 ** -16, f"loss {t}")

@@ -1,10 +1,14 @@
 // zq_ce_loss.hip -- softmax cross entropy of the vocabulary projection.
 //
 // The logits of a tile of tokens x vocabulary stay in the matrix product's
-// registers: the epilogue takes each token's largest sum m over the tile's columns, the
-// sum s of 2^(f (a - m)), f = unit log2 e, and the target's sum where it lies there.  A
-// second kernel joins the tiles' pairs,
-// (m, s) + (m', s') = (M, s 2^(f (m - M)) + s' 2^(f (m' - M))).
+// registers: the epilogue takes each token's largest sum m over the tile's columns but the
+// target's, the sum s of 2^(f (a - m)) over them, f = unit log2 e, and the target's sum
+// t where it lies there.  A second kernel joins the tiles' pairs,
+// (m, s) + (m', s') = (M, s 2^(f (m - M)) + s' 2^(f (m' - M))),
+// and forms  loss = log1p(s 2^(f (m - t))),  or where t < m
+//            loss = unit (m - t) + log(s + 2^(f (t - m))),
+// in which nothing cancels: the loss of a nearly sure token keeps its digits (taken as
+// lse - z it is off by half a unit of the logit's last place, 100 % of a loss of 1e-6).
 //
 // Bound by the matrix units with many tokens (16384 x 4096 x 32000 from int8 in 3.05 ms:
 // 1410 TFLOP/s, 0.07 ms of it the dequantization), by the read of w with few (one token,
@@ -79,7 +83,6 @@ struct Stats {
 #pragma unroll
         for (int i = 0; i < S::MI; ++i) {
             const uint32_t r = wm * (S::BM / S::WM) + i * 16 + (lane & 15), m = m0 + r;
-            float top = -__builtin_inff();
 #pragma unroll
             for (int j = 0; j < S::NI; ++j)
 #pragma unroll
@@ -88,11 +91,8 @@ struct Stats {
                     if (!whole)
                         acc[i][j][k] =
                             nw + j * 16 + k < N ? acc[i][j][k] : -__builtin_inff();
-                    top = __builtin_fmaxf(top, acc[i][j][k]);
                 }
-            top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-            // Few waves hold a target of their 16 rows.
+            // The target's sum stands apart.  Few waves hold a target of their 16 rows.
             const uint32_t target = m < M && targets[r] < N ? targets[r] : 0xFFFFFFFFu;
             const uint32_t off = target - nw;
             const bool here = off < S::NI * 16 && (off & 15) < 4;
@@ -101,11 +101,22 @@ struct Stats {
 #pragma unroll
                 for (int j = 0; j < S::NI; ++j)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        z = off == j * 16 + k ? acc[i][j][k] : z;
+                    for (int k = 0; k < 4; ++k) {
+                        const bool it = off == j * 16 + k;
+                        z = it ? acc[i][j][k] : z;
+                        acc[i][j][k] = it ? -__builtin_inff() : acc[i][j][k];
+                    }
                 if (here)
                     e.z_target[m] = z;
             }
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int j = 0; j < S::NI; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top = __builtin_fmaxf(top, acc[i][j][k]);
+            top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
             const float ref = reference(top);
             float sum = 0.0f;
 #pragma unroll
@@ -194,7 +205,6 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
         a.run[m] = mine;
         return;
     }
-    const float ref = reference(mine.x), log_sum = logf(mine.y);
     uint32_t t = m;
     if (a.list) {
         t = a.list[m];
@@ -207,8 +217,25 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
             return;
         }
     }
-    a.lse[t] = __builtin_fmaf(a.unit, ref, log_sum);
-    a.loss[t] = __builtin_fmaf(a.unit, ref - a.z_target[m], log_sum);
+    const float z = a.z_target[m];
+    float loss, lse;
+    if (__builtin_fabsf(z) < __builtin_inff() && mine.x < __builtin_inff()) {
+        if (z >= mine.x) {
+            loss = log1pf(mine.y * relative(factor, mine.x, z));
+            lse = __builtin_fmaf(a.unit, z, loss);
+        } else {
+            const float l = logf(mine.y + relative(factor, z, mine.x));
+            loss = __builtin_fmaf(a.unit, mine.x - z, l);
+            lse = __builtin_fmaf(a.unit, mine.x, l);
+        }
+    } else {  // infinite or NaN: what the formula gives
+        const float ref = reference(__builtin_fmaxf(mine.x, z));
+        const float sum = rebased(factor, mine, ref) + relative(factor, z, ref);
+        lse = __builtin_fmaf(a.unit, ref, logf(sum));
+        loss = lse - a.unit * z;
+    }
+    a.lse[t] = lse;
+    a.loss[t] = loss;
 }
 
 // Up to this many tokens the loss is formed for all of them, also those that are left
