@@ -158,8 +158,8 @@ size_t zq_ce_loss_workspace(size_t n_tok, uint64_t rows, uint64_t dim, uint64_t 
  *   ZQ_GRAD_WRITE: dw = G rounded to dw_dtype;  ZQ_GRAD_ADD: dw = fl(dw + G)
  *   rounded to dw_dtype.
  * Tokens that are left out have dx = +0 and no part in dw; their x, lse and
- * dloss are not used.  The logits are formed again, a piece of the vocabulary at
- * a time, and q is rounded to dtype before the two products (the matrix units
+ * dloss are not used.  The logits are formed again and rounded to binary32 as for the
+ * loss, a piece of the vocabulary at a time, and q is rounded to dtype before the two products (the matrix units
  * take 16-bit operands): an error of at most half a step of dtype per q, of the
  * size that the rounding of dx to dtype has (with 128 tokens or fewer q is kept in
  * two 16-bit parts, and the error is 2^-8 of that in bf16, 2^-11 in fp16).  It is

@@ -208,3 +208,31 @@ def test_infinite_and_nan_logits_of_targets_and_others(piece):
         want = torch.logsumexp(z[t], 0)
         near(lse[t:t + 1], want[None], 2.0 ** -16, f"lse {t}")
         near(loss[t:t + 1], (want - z[t, 300])[None], 2.0 ** -16, f"loss {t}")
+
+
+@pytest.mark.parametrize("scale", [1.0, -0.3])
+@pytest.mark.parametrize("n,rows", [(7, 257), (300, 1500)])
+def test_gradient_at_huge_finite_logits(n, rows, scale):
+    """Sums are exact (whole numbers times 2^30), lse is the largest logit rounded once: every
+    probability is 1 or 0, and with loss gradients that are powers of two every q is exact.
+    dx then rounds once, dw (fp32) not at all."""
+    x, w, ids = exact_operands(n, 64, rows, "bf16", 5, 1 if scale > 0 else -1)
+    ids = torch.where(torch.arange(n, device="cuda") % 3 == 0, some_ids(n, rows, 9), ids)
+    x, w = (x.float() * 2 ** 14).bfloat16(), (w.float() * 2 ** 16).bfloat16()
+    z = (x.double() @ w.double().t() * float(torch.tensor(scale))).float()
+    lse = z.max(1).values
+    got_lse = ce_loss(x, w, ids, scale)[1]
+    top = z.double().topk(2, 1).values
+    single = top[:, 0] - top[:, 1] > 0
+    near(got_lse[single], lse[single], 0.0, "lse")
+    dloss = torch.tensor([1.0, -0.5, 0.25], device="cuda")[torch.arange(n, device="cuda") % 3]
+    for piece in (0, 256):
+        dx, dw = ce_grad(x, w, ids, scale, lse, dloss, piece)
+        q = torch.exp(z.double() - lse[:, None].double())
+        assert bool(((q == 0) | (q == 1)).all())
+        q.scatter_add_(1, ids[:, None], torch.full_like(q[:, :1], -1.0))
+        q *= dloss[:, None].double()
+        want = q @ w.double() * float(torch.tensor(scale))
+        near(dx, want, (2.0 ** -8 + 2.0 ** -22) * want.abs(), "dx")
+        want = q.t() @ x.double() * float(torch.tensor(scale))
+        near(dw, want, 2.0 ** -22 * want.abs(), "dw")

@@ -39,7 +39,7 @@ struct Residual {
         uint32_t v0;
     };
 
-    // A token's target in the piece, its lse (in base 2), and its scaled loss gradient.
+    // A token's target in the piece, its lse, and its scaled loss gradient.
     struct Row {
         uint32_t target;
         float lse, g;
@@ -47,7 +47,7 @@ struct Residual {
     static __device__ __forceinline__ Row row(const Args& e, uint32_t M, uint32_t m0,
                                               uint32_t tid) {
         const uint32_t m = min(m0 + tid, M - 1);
-        return {e.t.target[m] - e.v0, base2(e.t.lse[m]), e.t.dloss[m] * e.t.scalars->up};
+        return {e.t.target[m] - e.v0, e.t.lse[m], e.t.dloss[m] * e.t.scalars->up};
     }
 
     template <class S>
@@ -62,7 +62,6 @@ struct Residual {
         if (threadIdx.x < S::BM)
             rows[threadIdx.x] = mine;
         __syncthreads();
-        const float factor = base2(e.scale);
         const uint32_t end = (N + kMmK - 1) / kMmK * kMmK;  // zeros from N up to here
         mm_rows<S>(
             acc, wm, wn, lane, lds, false, [](uint32_t, uint32_t) { return f4{0, 0, 0, 0}; },
@@ -74,7 +73,10 @@ struct Residual {
                 float q[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float p = exp2_of(__builtin_fmaf(factor, z[k], -t.lse));
+                    // The logit is rounded as the loss rounds it: of a sure token it is
+                    // lse, and p is 1, however large it is.  (In one fma of base 2 the
+                    // roundings of lse log2 e and of the factor stay in the exponent.)
+                    const float p = exp2_of(base2(e.scale * z[k] - t.lse));
                     q[k] = t.g * (n + k == t.target ? p - 1.0f : p);
                     q[k] = n + k < N ? q[k] : 0.0f;
                 }
