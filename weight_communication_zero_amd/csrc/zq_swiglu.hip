@@ -271,7 +271,8 @@ __device__ __forceinline__ void backward_tile(const SwigluGradArgs& a, uint64_t 
             float s, r;
             sigmoid(g, &s, &r);
             const float silu = g * s;
-            dg[j] = d[u][j] * v * s * (1.0f + g * r);
+            // The sigmoid's part, 1.1 at most, first: dh u alone may leave binary32.
+            dg[j] = d[u][j] * (s * (1.0f + g * r)) * v;
             du[j] = d[u][j] * silu;
             h[j] = silu * v;
         }
