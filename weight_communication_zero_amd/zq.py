@@ -662,6 +662,7 @@ def zq_linear_grad_int8(dy, codes, scales, block: int, grad, mode: int, workspac
     n_tok, dy_dim = _rows_dim("dy", dy)
     if dy_dim != out_dim:
         raise ValueError(f"dy has {dy_dim} columns, grad {out_dim} rows")
+    _width("codes", codes, in_dim, "grad")
     _need("dy", dy, n_tok * out_dim, _HALF)
     _need("codes", codes, n_tok * in_dim, _I8)
     _need("scales", scales, _blocks(n_tok * in_dim, block), _F32)
@@ -683,9 +684,28 @@ def ce_grad_workspace(n_tok: int, rows: int, dim: int, piece: int = 0) -> int:
     return lib.zq_ce_grad_workspace(n_tok, rows, dim, piece)
 
 
+def _width(name: str, t, dim: int, of: str) -> None:
+    """Refuses a tensor of two or more dimensions whose rows are not `dim` wide (its last
+    dimension, or the last few together): there may be enough elements all the same, and
+    they would be read at the wrong stride."""
+    if t is None or isinstance(t, int):
+        return
+    shape = t.shape
+    if len(shape) < 2 or shape[-1] == dim:
+        return
+    width = 1
+    for m in reversed(shape):
+        width *= m
+        if width >= dim or m == 0:
+            break
+    if width != dim and t.numel():
+        raise ValueError(f"{name} has {shape[-1]} columns, {of} {dim}")
+
+
 def _ce_loss(fn, x, w, w_args, rows: int, dim: int, ids, scale, loss, lse, workspace, piece,
              stream) -> None:
     n = ids.numel()
+    _width("x", x, dim, "the projection")
     _need("x", x, n * dim, _HALF)
     _need("ids", ids, n, _INDEX)
     _need("loss", loss, n, _F32)
@@ -698,8 +718,9 @@ def _ce_loss(fn, x, w, w_args, rows: int, dim: int, ids, scale, loss, lse, works
 
 def zq_ce_loss(x, w, ids, scale: float, loss, lse, workspace, piece: int = 0, stream=None) -> None:
     """Per-token softmax cross entropy of the logits scale * x w^T, which are never
-    kept: x (ids.numel() * dim) and w [rows, dim] bf16 or fp16, ids int32/int64 (one
-    outside the vocabulary leaves its token out: loss and lse 0), loss and lse fp32.
+    kept: x [..., dim] or flat (ids.numel() * dim) and w [rows, dim] bf16 or fp16, ids
+    int32/int64 (one outside the vocabulary leaves its token out: loss and lse 0), loss
+    and lse fp32.
     workspace: a uint8 tensor of ce_loss_workspace(tokens, rows, dim, piece) bytes;
     piece: vocabulary rows worked on at a time (0: the library's choice)."""
     rows, dim = _rows_dim("w", w)
@@ -721,6 +742,8 @@ def zq_ce_loss_int8(x, codes, scales, block: int, ids, scale: float, loss, lse, 
 def _ce_grad(fn, x, w, w_args, rows: int, dim: int, ids, scale, lse, dloss, dx, dw, mode, workspace,
              piece, stream) -> None:
     n = ids.numel()
+    for name, t in (("x", x), ("dx", dx), ("dw", dw)):
+        _width(name, t, dim, "the projection")
     _need("x", x, n * dim, _HALF)
     _need("ids", ids, n, _INDEX)
     _need("lse", lse, n, _F32)
