@@ -176,7 +176,8 @@ hipError_t launch(const CeArgs& a, int w_type, int dw_type, int mode, hipStream_
         to_w.a.a_cols = l.piece;
         to_w.a.b_cols = (uint32_t)l.kp;
         to_w.a.dyn_k = q_count;
-        to_w.o.out = (char*)a.dw + (uint64_t)v0 * a.dim * (dw_type == kF32 ? 4 : 2);
+        if (a.dw)
+            to_w.o.out = (char*)a.dw + (uint64_t)v0 * a.dim * (dw_type == kF32 ? 4 : 2);
         to_w.o.type = dw_type;
         to_w.o.add = mode == kGradAdd;
         if (a.dx && a.dw)
