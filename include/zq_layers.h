@@ -8,8 +8,8 @@
  *     (zq_quant_int8 of the activation, or the codes above);
  *   - softmax cross entropy of the vocabulary projection, worked through in
  *     pieces of the vocabulary so that the logits are never kept, with its
- *     gradient; the projection as 16-bit values or straight from the qwZ int8
- *     codes that the weight all-gather delivered.
+ *     gradient; the projection as 16-bit values or as the qwZ int8 codes that the
+ *     weight all-gather delivered, widened a piece at a time into the workspace.
  *
  * The conventions of zq.h and zq_train.h hold: device pointers on the current
  * device, work only enqueued on `stream`, nothing allocated or kept, validation
@@ -158,9 +158,9 @@ size_t zq_ce_loss_workspace(size_t n_tok, uint64_t rows, uint64_t dim, uint64_t 
  *   ZQ_GRAD_WRITE: dw = G rounded to dw_dtype;  ZQ_GRAD_ADD: dw = fl(dw + G)
  *   rounded to dw_dtype.
  * Tokens that are left out have dx = +0 and no part in dw; their x, lse and
- * dloss are not used.  The logits are formed again and rounded to binary32 as for the
- * loss, a piece of the vocabulary at a time, and q is rounded to dtype before the two products (the matrix units
- * take 16-bit operands): an error of at most half a step of dtype per q, of the
+ * dloss are not used.  The logits are formed again, a piece of the vocabulary at a
+ * time, and rounded to binary32 as for the loss; q is rounded to dtype before the two
+ * products (the matrix units take 16-bit operands): an error of at most half a step of dtype per q, of the
  * size that the rounding of dx to dtype has (with 128 tokens or fewer q is kept in
  * two 16-bit parts, and the error is 2^-8 of that in bf16, 2^-11 in fp16).  It is
  * the same for an fp32 dw, whose 32 bits are for adding many micro-batches.  In fp16, q is scaled by the

@@ -8,8 +8,11 @@
 // The second and third take their operands as they lie, by transposed reads from
 // LDS, so nothing is stored transposed; neither needs the other, so they share a launch.
 //
-// Bound by the matrix units: 16384 tokens, 4096 x 32000, take 9.7 ms in two pieces (1330
-// TFLOP/s over all), 8192 tokens, 2048 x 32000, with 10 % left out 2.29 ms.
+// Bound by the matrix units: 16384 tokens, 4096 x 32000, take 9.54 to 9.88 ms in two
+// pieces, by the card (1300 to 1350 TFLOP/s over all), 8192 tokens, 2048 x 32000, with
+// 10 % left out 2.26 to 2.36 ms.  Few tokens are bound by memory and by steps that wait
+// for each other: 64 tokens, 2048 x 32000, take 177 us, one read of w and one write of dw
+// 54 us at a copy's rate.
 #include "zq_ce.h"
 
 namespace zq {

@@ -10,9 +10,12 @@
 // in which nothing cancels: the loss of a nearly sure token keeps its digits (taken as
 // lse - z it is off by half a unit of the logit's last place, 100 % of a loss of 1e-6).
 //
-// Bound by the matrix units with many tokens (16384 x 4096 x 32000 from int8 in 3.05 ms:
-// 1410 TFLOP/s, 0.07 ms of it the dequantization), by the read of w with few (one token,
-// 4096 x 32000 in bf16: 56 us, the 262 MB at 5.4 TB/s and 6 us for the join).
+// Bound by the matrix units with many tokens (16384 x 4096 x 32000 from int8 in 3.04 to
+// 3.16 ms, by the card: 1360 to 1410 TFLOP/s, 0.07 ms of it the dequantization; the
+// differences before the factor are 0.02 of it), by the read of w with few (one token,
+// 4096 x 32000 in bf16: 56 us, of which 41 read the 262 MB, at 6.3 TB/s, and 6 join).  Few
+// tokens from codes wait for the widened copy of w, which is written and read again: one
+// token 119 us, where the codes alone are 27 us at a copy's rate.
 #include "zq_ce.h"
 
 namespace zq {
@@ -254,7 +257,8 @@ CeLayout layout(uint32_t n_tok, uint32_t rows, uint32_t dim, uint64_t piece) {
     l.kp = round_up(dim, kMmK);
     l.parts = 1;
     const uint64_t n_pad = round_up(n_tok, 256);
-    // The library's choice: 256 MiB each of staged rows and of pairs.
+    // The library's choice: at most 256 MiB of staged rows, and of pairs 128 (256-tiles),
+    // 256 or 512 MiB (small tiles).
     uint64_t most = piece ? round_up(std::min<uint64_t>(piece, rows), 256)
                           : std::min(((uint64_t)1 << 27) / l.kp, ((uint64_t)1 << 32) / n_pad);
     most = std::min(most, ((uint64_t)1 << 36) / n_pad);

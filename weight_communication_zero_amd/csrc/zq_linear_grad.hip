@@ -3,10 +3,10 @@
 //
 // Both operands lie with the summed index t outermost, so the product takes both as
 // transposed operands: no transposed copy is made.  The kept input is dequantized
-// once into the workspace (3 bytes an element) and read from there: of the 1.28 ms of
-// 16384 tokens, 11008 -> 4096, that takes 0.09 (540 MB at 5.9 TB/s) and the product 1.19
-// (1240 TFLOP/s; its 688 tiles are 2.7 rounds of the 256 CUs, so 10 % of the CUs' time
-// is idle in the third).
+// once into the workspace (3 bytes an element) and read from there: of the 1.25 to 1.32 ms
+// of 16384 tokens, 11008 -> 4096, that takes 0.09 (540 MB at 5.9 TB/s) and the product the
+// rest (1.23 ms in a trace: 1200 TFLOP/s; its 688 tiles are 2.7 rounds of the 256 CUs, so
+// 10 % of the CUs' time is idle in the third).
 #include "zq_mm_plan.h"
 #include "zq_stage.h"
 

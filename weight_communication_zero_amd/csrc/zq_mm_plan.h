@@ -37,7 +37,9 @@ inline uint64_t part_floats(const MmPlan& p, uint64_t M, uint64_t N) {
 
 // The tile and the splits of the least time by a simple model: the workgroups that a CU
 // works through, each of its steps of 64 k's and of what lies around them, and for a
-// split the partial sums' way to memory and back.  Fitted to measurements; the chosen
+// split the partial sums' way to memory and back.  Operands' bytes have no term in it: it
+// is fitted to products that the matrix units bound, and where one of few rows waits for
+// memory it may choose too many splits or too large a tile.  Measured; the chosen
 // and the next best of some products, in us (tile edge / splits):
 //   2048 x 2048 x 8192     128/2   73    256/4   75
 //   256 x 4096 x 16384     128/8   49    256/8   60
